@@ -9,9 +9,10 @@ fallback: if the library has not been built, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -97,6 +98,25 @@ def lib() -> ctypes.CDLL:
         L.gdattn_decode_noalloc.restype = ctypes.c_int
         L.gdattn_combine.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp]
         L.gdattn_combine.restype = ctypes.c_int
+        if hasattr(L, "gdattn_decode_sink"):
+            L.gdattn_sink_workspace_size.argtypes = [i32, i32, i32, descp, i32]
+            L.gdattn_sink_workspace_size.restype = sz
+            L.gdattn_decode_sink.argtypes = [vp, vp, vp, vp, i32, i32, i32, descp, i32, vp, vp,
+                                             vp, sz, vp]
+            L.gdattn_decode_sink.restype = ctypes.c_int
+            L.gdattn_prefix_workspace_size.argtypes = [i32, i32, i32, i32, descp]
+            L.gdattn_prefix_workspace_size.restype = sz
+            L.gdattn_decode_prefix.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32,
+                                               descp, vp, vp, vp, sz, vp]
+            L.gdattn_decode_prefix.restype = ctypes.c_int
+            L.gdattn_slot_map.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+            L.gdattn_slot_map.restype = ctypes.c_int
+            i64 = ctypes.c_int64
+            L.gdattn_cache_write.argtypes = [vp, vp, i64, vp, vp, i32, i32, descp, vp, vp, vp]
+            L.gdattn_cache_write.restype = ctypes.c_int
+            L.gdattn_cache_write_fp8.argtypes = [vp, vp, i64, vp, vp, i32, i32, descp, vp, vp,
+                                                 vp, vp, vp]
+            L.gdattn_cache_write_fp8.restype = ctypes.c_int
         L.gdattn_check_device_status.argtypes = [vp, vp]
         L.gdattn_check_device_status.restype = ctypes.c_int
         L.gdattn_read_probe.argtypes = [vp, sz, i32, vp, vp]
@@ -467,3 +487,264 @@ def read_probe(src: torch.Tensor, mode: int, sink: torch.Tensor, stream=None) ->
                                  _ptr(sink), _stream_handle(stream))
     if st != GDATTN_OK:
         raise GdattnError(st, "gdattn_read_probe")
+
+
+# ------------------------------------------------------ continuous batching
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on_device(device):
+    """Context in which ``device`` is the current one: the library launches on the
+    current device, so a call follows its tensors."""
+    index = device.index
+    if index is None or index == torch.cuda.current_device():
+        return _NO_SWITCH
+    return torch.cuda.device(device)
+
+
+def _check_tokens(q, k, v, seqlens, out, lse, desc) -> None:
+    """The arguments both continuous-batching attention calls share: q and out bf16
+    [T, B, Hq, D], lse fp32 [T, B, Hq] or None, caches spanning B sequences."""
+    T, B, Hq, D = q.shape
+    if Hq != desc.n_q_heads or D != desc.head_dim:
+        raise ValueError(f"q: heads and head_dim {(Hq, D)}, the descriptor has "
+                         f"{(int(desc.n_q_heads), int(desc.head_dim))}")
+    _check_layer(q, k, v, seqlens, out, lse, desc, T * B, B)
+
+
+def _check_workspace(workspace, device) -> None:
+    _dense(workspace, "workspace", (torch.uint8,), 0, device)
+
+
+def sink_workspace_size(batch: int, n_tokens: int, max_seqlen: int, desc: LayerDesc,
+                        n_sink: int) -> int:
+    return int(lib().gdattn_sink_workspace_size(int(batch), int(n_tokens), int(max_seqlen),
+                                                ctypes.byref(desc), int(n_sink)))
+
+
+def alloc_sink_workspace(batch: int, n_tokens: int, max_seqlen: int, desc: LayerDesc,
+                         n_sink: int, device="cuda", stream=None) -> torch.Tensor:
+    """A zeroed workspace for ``decode_sink`` calls of these sizes."""
+    return _zeroed_workspace(
+        lambda: sink_workspace_size(batch, n_tokens, max_seqlen, desc, n_sink),
+        "gdattn_sink_workspace_size", device, stream)
+
+
+def prefix_workspace_size(batch: int, n_tokens: int, max_seqlen: int, prefix_rows: int,
+                          desc: LayerDesc) -> int:
+    return int(lib().gdattn_prefix_workspace_size(int(batch), int(n_tokens), int(max_seqlen),
+                                                  int(prefix_rows), ctypes.byref(desc)))
+
+
+def alloc_prefix_workspace(batch: int, n_tokens: int, max_seqlen: int, prefix_rows: int,
+                           desc: LayerDesc, device="cuda", stream=None) -> torch.Tensor:
+    """A zeroed workspace for ``decode_prefix`` calls of these sizes."""
+    return _zeroed_workspace(
+        lambda: prefix_workspace_size(batch, n_tokens, max_seqlen, prefix_rows, desc),
+        "gdattn_prefix_workspace_size", device, stream)
+
+
+def _zeroed_workspace(size, what: str, device, stream) -> torch.Tensor:
+    with _on_device(torch.device(device)):
+        n = size()
+        if n == 0:
+            raise GdattnError(GDATTN_ERR_INVALID_ARG, what)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        workspace_init(ws, stream)
+    return ws
+
+
+def decode_sink_raw(q, k, v, seqlens, batch, n_tokens, max_seqlen, desc, n_sink, out, lse,
+                    workspace, workspace_bytes, stream) -> int:
+    """gdattn_decode_sink on raw addresses (ints); returns the status code."""
+    return lib().gdattn_decode_sink(q, k, v, seqlens, int(batch), int(n_tokens), int(max_seqlen),
+                                    ctypes.byref(desc), int(n_sink), out, lse, workspace,
+                                    int(workspace_bytes), stream)
+
+
+def decode_sink(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
+                seqlens: torch.Tensor, desc: LayerDesc, max_seqlen: int, n_sink: int,
+                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None):
+    """Sliding-window attention with n_sink pinned first tokens through
+    gdattn_decode_sink.  q bf16 [T, B, Hq, D]: token t of sequence b at position
+    L_b - T + t.  Returns (out, lse), token-major."""
+    T, B, Hq, D = q.shape
+    device = q.device
+    if out is None:
+        out = torch.empty((T, B, Hq, D), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=device)
+    _check_tokens(q, k, v, seqlens, out, lse, desc)
+    if workspace is None:
+        workspace = alloc_sink_workspace(B, T, max_seqlen, desc, n_sink, device, stream)
+    _check_workspace(workspace, device)
+    with _on_device(device):
+        st = decode_sink_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(seqlens), B, T, max_seqlen, desc,
+                             n_sink, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                             _stream_handle(stream))
+    if st != GDATTN_OK:
+        raise GdattnError(st, "gdattn_decode_sink")
+    return out, lse
+
+
+def decode_prefix_raw(q, k_prefix, v_prefix, prefix_len, prefix_rows, k, v, seqlens, batch,
+                      n_tokens, max_seqlen, desc, out, lse, workspace, workspace_bytes,
+                      stream) -> int:
+    """gdattn_decode_prefix on raw addresses (ints); returns the status code."""
+    return lib().gdattn_decode_prefix(q, k_prefix, v_prefix, prefix_len, int(prefix_rows), k, v,
+                                      seqlens, int(batch), int(n_tokens), int(max_seqlen),
+                                      ctypes.byref(desc), out, lse, workspace,
+                                      int(workspace_bytes), stream)
+
+
+def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: Optional[torch.Tensor],
+                  prefix_len: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
+                  seqlens: torch.Tensor, desc: LayerDesc, max_seqlen: int,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention behind a prefix that the batch shares, through gdattn_decode_prefix.
+
+    q bf16 [T, B, Hq, D]; k_prefix / v_prefix bf16 [prefix_rows, Hkv, D] (v_prefix None
+    when K = V); prefix_len int32 [1] on the device; k, v, seqlens the sequences' own
+    caches and lengths.  Returns (out, lse), token-major."""
+    T, B, Hq, D = q.shape
+    device = q.device
+    if out is None:
+        out = torch.empty((T, B, Hq, D), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=device)
+    _check_tokens(q, k, v, seqlens, out, lse, desc)
+    rows = k_prefix.shape[0]
+    _dense(k_prefix, "k_prefix", _BF16, rows * int(desc.n_kv_heads) * D, device)
+    if v_prefix is not None:
+        _dense(v_prefix, "v_prefix", _BF16, rows * int(desc.n_kv_heads) * D, device)
+    _dense(prefix_len, "prefix_len", _I32, 1, device)
+    if workspace is None:
+        workspace = alloc_prefix_workspace(B, T, max_seqlen, rows, desc, device, stream)
+    _check_workspace(workspace, device)
+    with _on_device(device):
+        st = decode_prefix_raw(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), rows,
+                               _ptr(k), _ptr(v), _ptr(seqlens), B, T, max_seqlen, desc, _ptr(out),
+                               _ptr(lse), _ptr(workspace), workspace.numel(),
+                               _stream_handle(stream))
+    if st != GDATTN_OK:
+        raise GdattnError(st, "gdattn_decode_prefix")
+    return out, lse
+
+
+class RowMap(NamedTuple):
+    """Where the packed rows of a step go (gdattn_slot_map), all int32."""
+
+    start: torch.Tensor  # [B + 1]: first row of each sequence, then the step's rows
+    seq: torch.Tensor    # [n_rows]: the row's sequence, -1 behind the last row
+    pos: torch.Tensor    # [n_rows]: its position in the sequence
+    slot: torch.Tensor   # [n_rows]: its slot in the sequence's cache, or -1
+
+
+def _row_map(batch: int, n_rows: int, device) -> RowMap:
+    flat = torch.empty(batch + 1 + 3 * n_rows, dtype=torch.int32, device=device)
+    return RowMap(*flat.split([batch + 1, n_rows, n_rows, n_rows]))
+
+
+def slot_map(seqlens: torch.Tensor, new_lens: torch.Tensor, n_rows: int, capacity: int,
+             n_sink: int = 0, out: Optional[RowMap] = None, stream=None) -> RowMap:
+    """gdattn_slot_map: the slots of a step in which new_lens[b] tokens join sequence
+    b (seqlens[b] long with them), packed into n_rows rows."""
+    B, device = seqlens.numel(), seqlens.device
+    n_rows = int(n_rows)
+    _dense(seqlens, "seqlens", _I32, B, device)
+    _dense(new_lens, "new_lens", _I32, B, device)
+    if n_rows < 0:
+        raise ValueError(f"n_rows: {n_rows}")
+    if out is None:
+        out = _row_map(B, n_rows, device)
+    else:
+        _dense(out.start, "out.start", _I32, B + 1, device)
+        for name in ("seq", "pos", "slot"):
+            _dense(getattr(out, name), f"out.{name}", _I32, n_rows, device)
+    with _on_device(device):
+        st = lib().gdattn_slot_map(_ptr(seqlens), _ptr(new_lens), B, n_rows, int(capacity),
+                                   int(n_sink), _ptr(out.start), _ptr(out.seq), _ptr(out.pos),
+                                   _ptr(out.slot), _stream_handle(stream))
+    if st != GDATTN_OK:
+        raise GdattnError(st, "gdattn_slot_map")
+    return out
+
+
+def _row_stride(rows: torch.Tensor, name: str, desc: LayerDesc, n_rows: int, device) -> int:
+    """Elements between the rows of a bf16 [n_rows, Hkv, D] tensor whose heads are
+    next to one another (a slice of a fused projection is)."""
+    if rows.dtype not in _BF16:
+        raise ValueError(f"{name}: dtype {rows.dtype}, expected torch.bfloat16")
+    H, D = int(desc.n_kv_heads), int(desc.head_dim)
+    if rows.dim() != 3 or tuple(rows.shape[1:]) != (H, D) or rows.shape[0] < n_rows:
+        raise ValueError(f"{name}: shape {tuple(rows.shape)}, expected at least {(n_rows, H, D)}")
+    if rows.stride(2) != 1 or (H > 1 and rows.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must be next to one another")
+    _on(rows, name, device)
+    return rows.stride(0) if rows.shape[0] > 1 else H * D
+
+
+def _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, dtypes):
+    """The arguments both cache writes share; returns (n_rows, batch, row stride)."""
+    device = k.device
+    n_rows, batch = row_slot.numel(), k.shape[0]
+    _dense(row_seq, "row_seq", _I32, n_rows, device)
+    _dense(row_slot, "row_slot", _I32, n_rows, device)
+    stride = _row_stride(k_rows, "k_rows", desc, n_rows, device)
+    _extent(k, "k", dtypes, _cache_elems(batch, desc), device)
+    if v_rows is not None and _row_stride(v_rows, "v_rows", desc, n_rows, device) != stride:
+        raise ValueError("v_rows: must have the row stride of k_rows")
+    if v is not None:
+        _extent(v, "v", dtypes, _cache_elems(batch, desc), device)
+    return n_rows, batch, stride
+
+
+def cache_write_raw(k_rows, v_rows, row_stride, row_seq, row_slot, n_rows, batch, desc, k, v,
+                    stream) -> int:
+    """gdattn_cache_write on raw addresses (ints); returns the status code."""
+    return lib().gdattn_cache_write(k_rows, v_rows, int(row_stride), row_seq, row_slot,
+                                    int(n_rows), int(batch), ctypes.byref(desc), k, v, stream)
+
+
+def cache_write(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_seq: torch.Tensor,
+                row_slot: torch.Tensor, desc: LayerDesc, k: torch.Tensor,
+                v: Optional[torch.Tensor] = None, stream=None) -> None:
+    """gdattn_cache_write: rows bf16 [n_rows, Hkv, D] (any row stride) into the caches
+    k, v [B, C, Hkv, D] by a slot map; v_rows and v None when K = V."""
+    n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, _BF16)
+    with _on_device(k.device):
+        st = cache_write_raw(_ptr(k_rows), _ptr(v_rows), stride, _ptr(row_seq), _ptr(row_slot),
+                             n_rows, batch, desc, _ptr(k), _ptr(v), _stream_handle(stream))
+    if st != GDATTN_OK:
+        raise GdattnError(st, "gdattn_cache_write")
+
+
+def cache_write_fp8_raw(k_rows, v_rows, row_stride, row_seq, row_slot, n_rows, batch, desc,
+                        k_codes, v_codes, k_scale, v_scale, stream) -> int:
+    """gdattn_cache_write_fp8 on raw addresses (ints); returns the status code."""
+    return lib().gdattn_cache_write_fp8(k_rows, v_rows, int(row_stride), row_seq, row_slot,
+                                        int(n_rows), int(batch), ctypes.byref(desc), k_codes,
+                                        v_codes, k_scale, v_scale, stream)
+
+
+def cache_write_fp8(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_seq: torch.Tensor,
+                    row_slot: torch.Tensor, desc: LayerDesc, k_codes: torch.Tensor,
+                    v_codes: Optional[torch.Tensor], k_scale: torch.Tensor,
+                    v_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """gdattn_cache_write_fp8: rows into the e4m3 caches [B, C, Hkv, D] (uint8 or
+    float8_e4m3fn) and their scales, fp32 [B, Hkv, C]."""
+    n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k_codes,
+                                         v_codes, _CODES)
+    scales = batch * int(desc.n_kv_heads) * int(desc.cache_capacity)
+    _dense(k_scale, "k_scale", _F32, scales, k_codes.device)
+    if v_scale is not None:
+        _dense(v_scale, "v_scale", _F32, scales, k_codes.device)
+    with _on_device(k_codes.device):
+        st = cache_write_fp8_raw(_ptr(k_rows), _ptr(v_rows), stride, _ptr(row_seq),
+                                 _ptr(row_slot), n_rows, batch, desc, _ptr(k_codes),
+                                 _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+                                 _stream_handle(stream))
+    if st != GDATTN_OK:
+        raise GdattnError(st, "gdattn_cache_write_fp8")

@@ -317,6 +317,154 @@ gdattn_status gdattn_decode_multi(const void *q, const void *k_cache, const void
                                   void *stream);
 
 /*
+ * ------------------------------------------------- continuous batching
+ * A step of a server that batches sequences as they come: rows of every
+ * sequence's new tokens are packed one after the other, written to the caches
+ * by a slot map, and attended with a window that keeps a few first tokens, or
+ * behind a prefix that the whole batch shares.  Library additions with no
+ * counterpart in the pages.
+ *
+ * These entry points take head_dim 256 and 512, any number of KV heads, up to
+ * 128 query heads per KV head, K = V or a separate V; other geometries return
+ * GDATTN_ERR_UNSUPPORTED.  They follow the conventions at the top of this file.
+ * The two attention calls start their workspace with the header described at
+ * gdattn_workspace_size, so one workspace (zeroed once by
+ * gdattn_workspace_init, at least as large as the largest size asked for) may
+ * serve them and the calls above in turn.  GDATTN_FLAG_EVEN_UNITS has no
+ * effect here: the planner always evens the work out from the device's lengths.
+ */
+
+/*
+ * Sliding-window attention whose first n_sink tokens stay visible ("sinks"):
+ * T query tokens per sequence, the last T positions of its context.  Query
+ * token t of sequence b sits at p = L_b - T + t and attends
+ *   [max(0, p + 1 - window), p + 1)  and  [0, min(n_sink, p + 1)),
+ * each position once.  T = 1 is a decode step, a small T a verify step, a large
+ * T a prompt chunk.
+ *
+ * The cache pins its first n_sink slots: position j lives in slot j below
+ * n_sink, and in slot n_sink + (j - n_sink) mod (C - n_sink) from there on.
+ * gdattn_slot_map and gdattn_cache_write fill it.  With n_sink = 0 this is
+ * gdattn_decode_multi's cache and step.
+ *
+ *  q         bf16 [T, batch, Hq, D] (token-major), device, read only
+ *  out       bf16 [T, batch, Hq, D];  lse: fp32 [T, batch, Hq] or NULL
+ *  n_tokens  T: 1 <= T <= 2^20, T <= max_seqlen
+ *  n_sink    0 <= n_sink < C
+ *  desc      window > 0, and C >= n_sink + window + T - 1 unless the cache never
+ *            wraps (C >= max_seqlen); otherwise GDATTN_ERR_INVALID_ARG
+ *  seqlens   L_b >= T with all T tokens in the cache, or 0 for a padding entry of
+ *            the batch: its out rows become 0, its lse -inf.  0 < L_b < T or
+ *            L_b < 0 latches GDATTN_ERR_DEVICE_SEQLEN, and tokens in front of
+ *            position 0 get 0 and -inf; so does a length whose window has left
+ *            the ring (its rows are invalid).
+ *  other arguments as gdattn_decode_multi
+ */
+size_t gdattn_sink_workspace_size(int32_t batch, int32_t n_tokens, int32_t max_seqlen,
+                                  const gdattn_layer_desc *desc, int32_t n_sink);
+
+gdattn_status gdattn_decode_sink(const void *q, const void *k_cache, const void *v_cache,
+                                 const int32_t *seqlens, int32_t batch, int32_t n_tokens,
+                                 int32_t max_seqlen, const gdattn_layer_desc *desc,
+                                 int32_t n_sink, void *out, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of a batch whose sequences share their first P tokens (a system
+ * prompt, a document): the prefix's K and V are stored once and its scores are
+ * computed for the whole batch together, so its rows are read once per call and
+ * not once per sequence.  Each sequence's cache holds its own tokens only, and
+ * seqlens counts those.  Query token t of sequence b sits r = L_b - T + t behind
+ * the prefix and attends the prefix positions j < P with j > P + r - window and
+ * its own positions j <= r with j > r - window (window 0: all of them).
+ *
+ *  q, out, lse   token-major as for gdattn_decode_sink
+ *  k_prefix      bf16 [prefix_rows][Hkv][D], device, read only
+ *  v_prefix      the same, or NULL when desc->kv_shared == 1
+ *  prefix_len    int32, device: P, 0 <= P <= prefix_rows (outside: clamped, and
+ *                GDATTN_ERR_DEVICE_SEQLEN).  Read like seqlens, so a captured
+ *                graph follows a prefix that grows within prefix_rows.
+ *  prefix_rows   >= 1: rows of the prefix tensors
+ *  k_cache, v_cache, desc: the sequences' own caches, position j (counted behind
+ *                the prefix) in slot j mod C
+ *  seqlens       L_b >= T, or 0 for a padding entry (out 0, lse -inf); other
+ *                lengths as for gdattn_decode_sink.  Without a window L_b <= C.
+ *  other arguments as gdattn_decode_sink
+ */
+size_t gdattn_prefix_workspace_size(int32_t batch, int32_t n_tokens, int32_t max_seqlen,
+                                    int32_t prefix_rows, const gdattn_layer_desc *desc);
+
+gdattn_status gdattn_decode_prefix(const void *q, const void *k_prefix, const void *v_prefix,
+                                   const int32_t *prefix_len, int32_t prefix_rows,
+                                   const void *k_cache, const void *v_cache,
+                                   const int32_t *seqlens, int32_t batch, int32_t n_tokens,
+                                   int32_t max_seqlen, const gdattn_layer_desc *desc, void *out,
+                                   float *lse, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * Where the packed rows of a step go.  new_lens[b] tokens of sequence b join it
+ * in this step (0: none; negative counts as 0), and seqlens[b] is its length
+ * with them; their rows follow one another, sequence after sequence.  One map
+ * serves every layer of one cache geometry.
+ *
+ *  seqlens, new_lens   int32 [batch], device
+ *  n_rows              rows of the outputs (>= 0); rows behind the step's last one
+ *                      get -1 everywhere, rows of the step beyond n_rows are left
+ *                      out (row_start[batch] tells)
+ *  cache_capacity, n_sink   C and the pinned slots, 0 <= n_sink < C
+ *  row_start  int32 [batch + 1]: first row of each sequence, then the step's rows
+ *             (sums above 2^31 - 1 read as that)
+ *  row_seq    int32 [n_rows]: the row's sequence
+ *  row_pos    int32 [n_rows]: its position in the sequence
+ *  row_slot   int32 [n_rows]: its slot in the sequence's cache, or -1 when a later
+ *             row of the same step takes that slot (a prompt longer than the
+ *             ring), or when the position is negative (new_lens above seqlens)
+ */
+gdattn_status gdattn_slot_map(const int32_t *seqlens, const int32_t *new_lens, int32_t batch,
+                              int32_t n_rows, int32_t cache_capacity, int32_t n_sink,
+                              int32_t *row_start, int32_t *row_seq, int32_t *row_pos,
+                              int32_t *row_slot, void *stream);
+
+/*
+ * Write K and V rows into the caches of one layer by a slot map:
+ * cache[row_seq[i]][row_slot[i]] = rows[i].  Rows whose sequence is not in
+ * [0, batch) or whose slot is not in [0, C) are skipped; nothing else in the
+ * caches is written.  Two rows with the same sequence and slot leave either one
+ * of them there, piecewise; a slot map has no such rows.
+ *
+ *  k_rows      bf16, row i at k_rows + i * row_stride elements: [Hkv][D], the
+ *              heads next to one another (a slice of a fused projection)
+ *  v_rows      the same, or NULL when desc->kv_shared == 1
+ *  row_stride  >= Hkv * D and a multiple of 8
+ *  row_seq, row_slot   int32 [n_rows], device; n_rows may be 0
+ *  desc        geometry, capacity and cache_batch_stride; window, scale, softcap
+ *              and flags are checked but not used
+ *  k_cache, v_cache    as gdattn_decode's, written
+ */
+gdattn_status gdattn_cache_write(const void *k_rows, const void *v_rows, int64_t row_stride,
+                                 const int32_t *row_seq, const int32_t *row_slot, int32_t n_rows,
+                                 int32_t batch, const gdattn_layer_desc *desc, void *k_cache,
+                                 void *v_cache, void *stream);
+
+/*
+ * gdattn_cache_write into an fp8 cache (gdattn_decode_fp8 reads it): each row of
+ * each KV head gets the scale s = max |x| / 448 and the codes e4m3(x / s), both
+ * quotients rounded to fp32, the code to the nearest (ties to even); a row of
+ * zeros gets scale 0 and codes 0.  Rows must be finite.
+ *
+ *  k_codes, v_codes   e4m3 bytes; cache_batch_stride counts bytes and is a
+ *                     multiple of 16
+ *  k_scale, v_scale   fp32 [batch][Hkv][C], written at the rows' slots
+ *  other arguments as gdattn_cache_write
+ */
+gdattn_status gdattn_cache_write_fp8(const void *k_rows, const void *v_rows, int64_t row_stride,
+                                     const int32_t *row_seq, const int32_t *row_slot,
+                                     int32_t n_rows, int32_t batch, const gdattn_layer_desc *desc,
+                                     void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                                     void *stream);
+
+/*
  * gdattn_decode without a caller workspace.  A library addition with no
  * counterpart in the pages; it computes exactly what gdattn_decode computes.
  *
