@@ -1,0 +1,594 @@
+// Attention of blocks of query rows over cache rows, on the 5th-generation tensor
+// cores: the kernel of gdattn_decode_sink and gdattn_decode_prefix.
+//
+// A block is up to 128 query rows of one KV head: tokens of one sequence times
+// the query heads of the group, or (token, sequence) pairs of the batch times the
+// group, over the shared prefix.  Per tile of 64 cache rows
+//
+//   S[128 x 64]   = Q[128 x D] . K_tile^T[D x 64]
+//   O[128 x D]   += P_hi[128 x 64] . V_tile[64 x D] + P_lo[128 x 64] . V_tile[64 x D]
+//
+// with the running maximum and sum of a softmax in one pass.  Every TMEM lane is a
+// query row, so a softmax thread owns a row and needs no exchange with others.
+// Weights are stored as bf16 plus the bf16 remainder (truncated; 2^-14 relative).
+// A row's reference maximum moves only when a score exceeds it by 2^8; the thread
+// then rescales its O row in TMEM.
+//
+// head_dim 512 (NH = 2): O alone would fill tensor memory, so a block runs on a
+// cluster of two CTAs, each with 256 of the dims of Q, K, V and O.  Each computes
+// the scores' partial sum over its dims and sends it to the other through
+// distributed shared memory (32 KiB a tile and direction); both then add the two
+// parts in the same way, so their softmax decisions agree bit for bit.  A cache
+// row crosses HBM once and no product is computed twice.
+//
+// Work split: rows_chunks.cuh lays all tiles end to end and gives each worker (CTA
+// or pair) an equal chunk; loads run ahead across units.  Whole units are written
+// directly (sinks), pieces as normalised fp32 partials plus log2-sum-exp, which
+// rows_merge.cuh joins.
+//
+// Shared memory (1 CTA per SM): Q blocks (64 KiB; two buffers when a block's rows
+// fill at most half), a ring of 32 KiB tiles (five for NH = 1; three for NH = 2 beside
+// two 32 KiB score exchange buffers).  K and V tiles take turns in the ring; with
+// K = V a tile serves both products.  Partial tiles are fetched in 16-row boxes.
+//
+// Warps: 0 loads tiles, 3 loads Q, 1 issues Q.K and owns TMEM, 2 issues P.V, 4-7
+// run the softmax (rows 32 s .. 32 s + 31 in warp 4 + s).  Every wait is bounded.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "../ptx.cuh"
+#include "rows_chunks.cuh"
+#include "rows_plan.cuh"
+#include "rows_ptx.cuh"
+
+namespace gdattn {
+
+template <int NH>
+struct RowsConfig {
+  static constexpr int DH = 256;                    // dims per CTA
+  static constexpr int D = DH * NH;
+  static constexpr int M = 128;                     // query rows per block
+  static constexpr int TILE = kRowTile;
+  static constexpr int BOXB = TILE * 128;           // 64 rows x 64 dims: 8 KiB
+  static constexpr int TB = BOXB * (DH / 64);       // a tile: 32 KiB
+  static constexpr int NST = NH == 1 ? 5 : 3;       // ring
+  static constexpr int QB = 64 * 1024;
+  static constexpr int XB = M * TILE * 4;           // score exchange buffer: 32 KiB
+  static constexpr int OFF_KV = QB;                 // Q first: its MMA reads run past short blocks
+  static constexpr int OFF_X = OFF_KV + NST * TB;
+  static constexpr int OFF_BAR = OFF_X + (NH == 1 ? 0 : 2 * XB);
+  static constexpr int SMEM = OFF_BAR + 1024 + 1024;
+  static constexpr int kThreads = 256;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t S_COL = 0;              // 2 buffers x 64
+  static constexpr uint32_t P_COL = 128;            // 2 buffers x (32 + 32)
+  static constexpr uint32_t O_COL = 256;            // 256
+};
+static_assert(RowsConfig<1>::SMEM <= 227 * 1024 && RowsConfig<2>::SMEM <= 227 * 1024,
+              "shared memory budget");
+
+struct RowsParams {
+  RowsGeom g;
+  uint16_t *out;       // bf16 [T][B][Hq][D]
+  float *lse;          // [T][B][Hq] or null
+  float *own_o, *own_lse;  // partials of own units, rs rows a slot
+  float *pre_o, *pre_lse;  // partials of prefix units, rp rows a slot
+  uint32_t *status;
+  int32_t workers;
+  int32_t rs, rp;      // rows of a slot
+  int32_t q_stride;    // bytes between the 64-dim chunks of a Q block (1 KiB multiple)
+  int32_t q_bufs;      // Q buffers (1 or 2)
+  int32_t q_bytes_own, q_bytes_pre;  // bytes of a 64-dim chunk that TMA writes
+  float qscale;        // scale * log2(e), or scale / cap with a soft-cap
+  float post;          // cap * log2(e), or 0
+  int32_t test_withhold;
+};
+
+// The tensor maps of a call: caches and prefix in boxes of 64 rows and of 16,
+// q by (token, sequence x head) and by (token x sequence, head).
+struct RowsMaps {
+  CUtensorMap k, v, k16, v16;
+  CUtensorMap pk, pv, pk16, pv16;
+  CUtensorMap q_own, q_pre;
+};
+
+template <int NH, bool SHARED>
+__global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
+    rows_attn_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
+  using Cfg = RowsConfig<NH>;
+  constexpr int DH = Cfg::DH, NST = Cfg::NST, TILE = Cfg::TILE;
+  constexpr int EPT = SHARED ? 1 : 2;  // ring entries per tile
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *qs = smem;
+  uint8_t *kv = smem + Cfg::OFF_KV;
+  float4 *xs = reinterpret_cast<float4 *>(smem + Cfg::OFF_X);  // [2][16 column quads][128 rows]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
+  uint64_t *full = bars;           // [5] TMA -> Q.K, P.V (and the softmax, for partial tiles)
+  uint64_t *empty = bars + 5;      // [5] Q.K / P.V -> TMA
+  uint64_t *sfull = bars + 10;     // [2] Q.K -> softmax
+  uint64_t *sempty = bars + 12;    // [2] softmax -> Q.K
+  uint64_t *qfull = bars + 14;     // [2] TMA -> Q.K
+  uint64_t *qempty = bars + 16;    // [2] Q.K -> TMA
+  uint64_t *pfull = bars + 18;     // [2] softmax -> P.V
+  uint64_t *odone = bars + 20;     // [2] P.V -> softmax
+  uint64_t *drain = bars + 22;     // [2] the MMA warps: all their MMAs are done
+  uint64_t *xfull = bars + 24;     // [2][4] peer's softmax warp -> this one: its scores are here
+  uint64_t *xfree = bars + 32;     // [2][4] peer's softmax warp: read what this one sent
+  uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 40);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 41);
+  RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 42);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const RowsGeom &g = p.g;
+  const int32_t worker = static_cast<int32_t>(blockIdx.x) / NH;
+  const int rank = NH == 1 ? 0 : static_cast<int>(blockIdx.x) % NH;  // this CTA's dims
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sempty[s], 4);
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qempty[s], 1);
+      mbar_init(&pfull[s], 4);
+      mbar_init(&odone[s], 1);
+      mbar_init(&drain[s], 1);
+    }
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xfree[s], 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 3 && lane == 0) {
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.q_own);
+    if (g.prefix_len != nullptr) {
+      prefetch_tensormap(&maps.pk);
+      prefetch_tensormap(&maps.q_pre);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_base_smem, Cfg::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0) {
+    const RowsPlan pl = plan_rows(g, worker, p.workers);
+    if (lane == 0) *plan_smem = pl;
+  }
+  grid_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (NH == 2) cluster_sync();  // the peer's barriers are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_smem;
+  const RowsPlan plan = *plan_smem;
+  RowSegments segs;
+  segs.init(g, plan);
+  RowSegment seg;
+
+  if (warp == 0) {
+    // --------------------------------------------------------- tile loads
+    grid_dependency_wait();
+    if (plan.bad && worker == 0 && rank == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
+    const uint64_t pol = l2_evict_first_policy();
+    bool ok = true;
+    uint32_t e = 0;  // ring entries so far
+    while (ok && segs.next(g, seg)) {
+      for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
+        const RowTile tile = unit_tile(seg.u, t);
+#pragma unroll
+        for (int part = 0; part < EPT; ++part) {
+          const int st = e % NST;
+          if (e >= NST) ok = mbar_wait(&empty[st], ((e / NST) - 1) & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (!(p.test_withhold && e == 0) && elect_one()) {
+            const bool is_v = part == 1;
+            const bool big = tile.ntok > 48;
+            const int boxes = big ? 1 : (tile.ntok + 15) / 16;
+            const CUtensorMap *map =
+                seg.prefix ? (big ? (is_v ? &maps.pv : &maps.pk) : (is_v ? &maps.pv16 : &maps.pk16))
+                           : (big ? (is_v ? &maps.v : &maps.k) : (is_v ? &maps.v16 : &maps.k16));
+            uint8_t *dst = kv + st * Cfg::TB;
+            if (boxes == 0) {
+              mbar_arrive(&full[st]);  // a tile of no rows: nothing to load
+            } else {
+              mbar_arrive_expect_tx(&full[st],
+                                    static_cast<uint32_t>((big ? TILE : 16 * boxes) * 2 * DH));
+              for (int q = 0; q < boxes; ++q)
+#pragma unroll
+                for (int j = 0; j < DH / 64; ++j)
+                  tma_load_4d(dst + j * Cfg::BOXB + q * 2048, map, rank * DH + 64 * j, seg.x,
+                              tile.slot + 16 * q, seg.b, &full[st], pol);
+            }
+          }
+          __syncwarp();
+          ++e;
+        }
+      }
+    }
+    // Never leave with copies in flight into shared memory.
+    volatile int no_abort = 0;
+    for (uint32_t f = e > NST ? e - NST : 0; f < e; ++f)
+      if (!(p.test_withhold && f == 0))
+        mbar_wait(&full[f % NST], (f / NST) & 1, &no_abort, p.status);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ Q loads
+    grid_dependency_wait();
+    bool ok = true;
+    uint32_t n = 0;  // blocks so far
+    while (ok && segs.next(g, seg)) {
+      const uint32_t buf = n % p.q_bufs, use = n / p.q_bufs;
+      if (use > 0) ok = mbar_wait(&qempty[buf], (use - 1) & 1, abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (elect_one()) {
+        uint8_t *dst = qs + buf * 4 * p.q_stride;
+        mbar_arrive_expect_tx(&qfull[buf], 4 * (seg.prefix ? p.q_bytes_pre : p.q_bytes_own));
+#pragma unroll
+        for (int j = 0; j < DH / 64; ++j) {
+          if (seg.prefix)
+            tma_load_tokens(dst + j * p.q_stride, &maps.q_pre, rank * DH + 64 * j, seg.x * g.group,
+                        seg.qb * g.qt_pre, &qfull[buf]);
+          else
+            tma_load_tokens(dst + j * p.q_stride, &maps.q_own, rank * DH + 64 * j,
+                        (seg.b * g.n_kv_heads + seg.x) * g.group, seg.qb * g.qt_seq, &qfull[buf]);
+        }
+      }
+      __syncwarp();
+      ++n;
+    }
+    volatile int no_abort = 0;
+    const uint32_t bufs = static_cast<uint32_t>(p.q_bufs);
+    for (uint32_t f = n > bufs ? n - bufs : 0; f < n; ++f)
+      mbar_wait(&qfull[f % bufs], (f / bufs) & 1, &no_abort, p.status);
+  } else if (warp == 1) {
+    // --------------------------------------------------------- Q.K MMAs
+    const uint32_t idesc = idesc_bf16_f32(128, TILE, false, false);
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(qs), 16, 1024);  // K-major
+    const uint64_t kdesc = smem_desc_sw128(smem_u32(kv), 16, 1024);  // K-major
+    bool ok = true;
+    uint32_t i = 0, n = 0;
+    while (ok && segs.next(g, seg)) {
+      const uint32_t buf = n % p.q_bufs, use = n / p.q_bufs;
+      ok = mbar_wait(&qfull[buf], use & 1, abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      const uint32_t qoff = (buf * 4 * p.q_stride) >> 4, qstep = p.q_stride >> 4;
+      for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
+        const uint32_t e = i * EPT;
+        const int st = e % NST, sb = i & 1;
+        ok = mbar_wait(&full[st], (e / NST) & 1, abort_flag, p.status);
+        if (ok && i >= 2) ok = mbar_wait(&sempty[sb], ((i >> 1) - 1) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < DH / 64; ++j)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16(tmem + Cfg::S_COL + sb * TILE, qdesc + qoff + j * qstep + kk * 2,
+                          kdesc + ((st * Cfg::TB + j * Cfg::BOXB + kk * 32) >> 4), idesc,
+                          (j | kk) != 0);
+          tc_commit(&sfull[sb]);
+          if (!SHARED) tc_commit(&empty[st]);
+          if (t + 1 == seg.t1) tc_commit(&qempty[buf]);
+        }
+        __syncwarp();
+        ++i;
+      }
+      ++n;
+    }
+    if (elect_one()) tc_commit(&drain[0]);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(&drain[0], 0, &no_abort, p.status);
+  } else if (warp == 2) {
+    // --------------------------------------------------------- P.V MMAs
+    const uint32_t idesc = idesc_bf16_f32(128, DH, false, true);
+    // V tile as the MN-major B operand: 64-dim chunks BOXB apart, 8 rows per 1 KiB
+    const uint64_t vdesc = smem_desc_sw128(smem_u32(kv), Cfg::BOXB, 1024);
+    bool ok = true;
+    uint32_t i = 0;
+    while (ok && segs.next(g, seg)) {
+      for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
+        const uint32_t e = i * EPT + EPT - 1;
+        const int st = e % NST, pb = i & 1;
+        ok = mbar_wait(&pfull[pb], (i >> 1) & 1, abort_flag, p.status);
+        if (ok) ok = mbar_wait(&full[st], (e / NST) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          // A = P from tensor memory: 16 rows' weights are 8 columns of bf16 pairs.
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int kk = 0; kk < TILE / 16; ++kk)
+              tc_mma_bf16_ta(tmem + Cfg::O_COL, tmem + Cfg::P_COL + pb * 64 + half * 32 + kk * 8,
+                             vdesc + ((st * Cfg::TB + kk * 2048) >> 4), idesc,
+                             !(t == seg.t0 && half == 0 && kk == 0));
+          tc_commit(&odone[pb]);
+          tc_commit(&empty[st]);
+        }
+        __syncwarp();
+        ++i;
+      }
+    }
+    if (elect_one()) tc_commit(&drain[1]);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(&drain[1], 0, &no_abort, p.status);
+  } else {
+    // --------------------------------------------------------- softmax
+    grid_dependency_wait();  // outputs are written below
+    const int qd = warp & 3;
+    const int t128 = threadIdx.x - 128;
+    const int r = 32 * qd + lane;  // this thread's query row (TMEM lane)
+    const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
+    const int32_t Hq = g.n_kv_heads * g.group;
+    bool ok = true;
+    uint32_t i = 0;
+    uint32_t xi = 0;  // score exchanges so far (tiles of blocks with rows in this warp)
+    // The P.V of tile tt (and so every earlier one: they complete in order) has
+    // completed.  Each odone barrier's phases are consumed in order, and a
+    // barrier never runs two phases ahead of its waiter (the P.V two tiles on
+    // needs this warp's next P), so the parity waits cannot alias.
+    uint32_t done0 = 0, done1 = 0;  // phases consumed on odone[0], odone[1]
+    auto ensure_pv = [&](uint32_t tt) {
+      const uint32_t ph = tt >> 1;
+      if (tt & 1) {
+        for (; done1 <= ph; ++done1)
+          if (ok && !mbar_wait(&odone[1], done1 & 1, abort_flag, p.status)) ok = false;
+      } else {
+        for (; done0 <= ph; ++done0)
+          if (ok && !mbar_wait(&odone[0], done0 & 1, abort_flag, p.status)) ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    while (segs.next(g, seg)) {
+      // The row: its token, sequence and head, and the positions it sees.
+      const int32_t qt = seg.prefix ? g.qt_pre : g.qt_seq;
+      const int32_t all = seg.prefix ? g.tokens * g.batch : g.tokens;  // of this axis
+      const int32_t nrow = imin32(qt, all - seg.qb * qt) * g.group;
+      const int32_t tq = r / g.group, h = r - tq * g.group;
+      const bool row_ok = r < nrow;
+      RowRange rg = {0, 0, 0};
+      int32_t tok = 0, b = 0;
+      if (row_ok) {
+        const int32_t a = seg.qb * qt + tq;
+        if (seg.prefix) {
+          tok = a / g.batch;
+          b = a - tok * g.batch;
+          rg = prefix_row_range(g, __ldg(g.seqlens + b), tok, plan.prefix_len);
+        } else {
+          tok = a;
+          b = seg.b;
+          rg = own_row_range(g, seg.L, tok);
+        }
+      }
+      const bool act = 32 * qd < nrow;  // the warp has rows (warp-uniform)
+      float m_ref = -INFINITY, l = 0.f;
+      for (int32_t t = seg.t0; t < seg.t1; ++t) {
+        const RowTile tile = unit_tile(seg.u, t);
+        const int sb = i & 1;
+        float s[TILE];
+        if (ok && !mbar_wait(&sfull[sb], (i >> 1) & 1, abort_flag, p.status)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && act) {
+          tc_fence_after();
+          tmem_ld64(tmem + lane_base + Cfg::S_COL + sb * TILE, s);
+          tc_fence_before();
+        } else {
+#pragma unroll
+          for (int c = 0; c < TILE; ++c) s[c] = 0.f;
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&sempty[sb]);
+        if (NH == 2 && act) {
+          // The peer holds the scores' other half of the dims: swap and add.
+          const int xb = xi & 1;
+          if (ok && xi >= 2 &&
+              !mbar_wait_cluster(&xfree[xb * 4 + qd], ((xi >> 1) - 1) & 1, abort_flag, p.status))
+            ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            const uint32_t dst =
+                peer_smem(smem_u32(xs + xb * (Cfg::XB / 16) + r), static_cast<uint32_t>(rank ^ 1));
+#pragma unroll
+            for (int c = 0; c < TILE / 4; ++c)
+              st_peer_v4(dst + c * (Cfg::M * 16), s[4 * c], s[4 * c + 1], s[4 * c + 2],
+                         s[4 * c + 3]);
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_peer(peer_smem(smem_u32(&xfull[xb * 4 + qd]), rank ^ 1));
+            if (!mbar_wait_cluster(&xfull[xb * 4 + qd], (xi >> 1) & 1, abort_flag, p.status))
+              ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < TILE / 4; ++c) {
+              const float4 o = xs[xb * (Cfg::XB / 16) + c * Cfg::M + r];
+              s[4 * c] += o.x;
+              s[4 * c + 1] += o.y;
+              s[4 * c + 2] += o.z;
+              s[4 * c + 3] += o.w;
+            }
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_peer(peer_smem(smem_u32(&xfree[xb * 4 + qd]), rank ^ 1));
+          }
+          ++xi;
+        }
+        if (act) {
+          // Scores in log2 units (scale, then the soft-cap if there is one).
+          if (p.post != 0.f) {
+#pragma unroll
+            for (int c = 0; c < TILE; ++c) s[c] = p.post * tanhf(s[c] * p.qscale);
+          } else {
+#pragma unroll
+            for (int c = 0; c < TILE; ++c) s[c] *= p.qscale;
+          }
+          // Column c is position tile.pos + c.  A tile that every row of the warp
+          // sees in full needs no mask.
+          const bool inside = ok && tile.ntok == TILE && tile.pos >= rg.lo &&
+                              tile.pos + TILE <= rg.hi;
+          if (!__all_sync(0xffffffffu, inside)) {
+            const int32_t c_lo = rg.lo - tile.pos, c_pin = rg.pin - tile.pos;
+            const int32_t c_hi = ok ? imin32(rg.hi - tile.pos, tile.ntok) : 0;
+#pragma unroll
+            for (int c = 0; c < TILE; ++c)
+              s[c] = ((c >= c_lo || c < c_pin) && c < c_hi) ? s[c] : -INFINITY;
+          }
+          float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < TILE; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          // Move the reference of a row when a score outgrew it.  The TMEM loads
+          // and stores are warp-wide: rows whose reference stays multiply by 1.
+          const bool mine = mx > m_ref + kRefStep;
+          if (__any_sync(0xffffffffu, mine)) {
+            float alpha = 1.f;
+            if (mine) {
+              alpha = m_ref == -INFINITY ? 0.f : exp2f(m_ref - mx);
+              l *= alpha;
+              m_ref = mx;
+            }
+            if (t > seg.t0) {
+              ensure_pv(i - 1);
+              if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < DH / 32; ++cb) {
+                  float o[32];
+                  tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) o[q] *= alpha;
+                  tmem_store32_wait(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+                }
+              }
+            }
+          }
+          // Weights: bf16 pairs (column j holds rows 2j, 2j + 1) and remainders, both
+          // truncated (the upper halves of the fp32 bits; the remainder is exact in
+          // fp32 before its own truncation): 2^-14 relative.  A row without any score
+          // yet (reference -inf) has only masked columns here: 2^-inf = 0.
+          const float mr = m_ref == -INFINITY ? 0.f : m_ref;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          float wh[TILE / 2], wl[TILE / 2];
+#pragma unroll
+          for (int j = 0; j < TILE / 2; ++j) {
+            const float pa = ex2_approx(s[2 * j] - mr);
+            const float pb = ex2_approx(s[2 * j + 1] - mr);
+            l4[j & 3] += pa + pb;
+            const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
+            const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
+            const float rb = pb - __uint_as_float(ub & 0xFFFF0000u);
+            wh[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
+            wl[j] = __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          if (i >= 2) ensure_pv(i - 2);  // the P.V of tile i - 2 read this P buffer
+          if (ok) {
+            tmem_store32_wait(tmem + lane_base + Cfg::P_COL + sb * 64, wh);
+            tmem_store32_wait(tmem + lane_base + Cfg::P_COL + sb * 64 + 32, wl);
+          }
+        } else if (i >= 2) {
+          ensure_pv(i - 2);  // keeps this warp's arrivals in the barrier's phase
+        }
+        if (ok && tile.ntok < TILE) {
+          // Rows behind the tile's end hold other slots, or what the ring held
+          // before (possibly NaN, which a weight of 0 would not silence): clear
+          // them.  With K = V the tile's Q.K is done: its S was read.
+          const uint32_t e = i * EPT + EPT - 1;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&full[e % NST], (e / NST) & 1, abort_flag, p.status));
+          if (ok) {
+            uint8_t *vt = kv + (e % NST) * Cfg::TB;
+            const int per_box = (TILE - tile.ntok) * 8;
+#pragma unroll 1
+            for (int box = 0; box < DH / 64; ++box)
+              for (int q = t128; q < per_box; q += 128)
+                *reinterpret_cast<uint4 *>(vt + box * Cfg::BOXB + (tile.ntok + (q >> 3)) * 128 +
+                                           (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();  // the cleared rows, for the tensor core
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&pfull[sb]);
+        ++i;
+      }
+      // --- the rows' output: final, or a partial of its unit.
+      ensure_pv(i - 1);
+      if (!act) continue;
+      const bool have_o = ok;  // warp-uniform
+      const float inv = (have_o && l > 0.f) ? __fdividef(1.f, l) : 0.f;
+      const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
+      const bool final_rows = g.prefix_len == nullptr && seg.whole();
+      const int64_t orow =
+          (static_cast<int64_t>(tok) * g.batch + b) * Hq + seg.x * g.group + h;
+      const int64_t prow =
+          partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens) *
+              (seg.prefix ? p.rp : p.rs) + r;
+      uint16_t *dst = p.out + orow * Cfg::D + rank * DH;
+      float *part = (seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D + rank * DH;
+      if (have_o) tc_fence_after();
+#pragma unroll 1
+      for (int cb = 0; cb < DH / 32; ++cb) {
+        float o[32];
+        if (have_o) {
+          tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = 0.f;
+        }
+        if (row_ok && final_rows) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 8) {
+            uint4 pk;
+            pk.x = pack_bf16x2(o[q] * inv, o[q + 1] * inv);
+            pk.y = pack_bf16x2(o[q + 2] * inv, o[q + 3] * inv);
+            pk.z = pack_bf16x2(o[q + 4] * inv, o[q + 5] * inv);
+            pk.w = pack_bf16x2(o[q + 6] * inv, o[q + 7] * inv);
+            *reinterpret_cast<uint4 *>(dst + cb * 32 + q) = pk;
+          }
+        } else if (row_ok) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            *reinterpret_cast<float4 *>(part + cb * 32 + q) =
+                make_float4(o[q] * inv, o[q + 1] * inv, o[q + 2] * inv, o[q + 3] * inv);
+        }
+      }
+      tc_fence_before();
+      if (row_ok && rank == 0) {
+        if (!final_rows)
+          (seg.prefix ? p.pre_lse : p.own_lse)[prow] = lse2;
+        else if (p.lse != nullptr)
+          p.lse[orow] = l > 0.f ? lse2 * kLn2 : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (NH == 2) cluster_sync();  // neither CTA leaves while the other may write into it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace gdattn

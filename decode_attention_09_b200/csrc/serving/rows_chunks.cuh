@@ -1,0 +1,215 @@
+// Split of a call's tiles over the CTAs (or CTA pairs) of the grid.
+//
+// All units' tiles are laid end to end: first the prefix units, unit
+// u = x * npb + pb (KV head x, prefix block pb), then the own units, unit
+// y * Hkv + x for pair y = b * nqb + qb (sequence b, its block qb).  The whole is
+// cut into equal chunks, one per worker (a CTA or a CTA pair), whatever the mix
+// of lengths: the lengths are read on the device, so a captured graph follows
+// them and the host never waits.  The piece of a unit in a chunk is a segment.
+#pragma once
+
+#include <cstdint>
+
+#include "../ptx.cuh"
+#include "rows_plan.cuh"
+
+namespace gdattn {
+
+struct RowsPlan {
+  int64_t total;      // tiles
+  int64_t chunk;      // tiles per worker
+  int64_t cs, ce;     // this worker's tiles
+  int64_t prefix_all; // tiles of all prefix units
+  int64_t y_start;    // first tile of pair y
+  int32_t y;          // the own pair that tile max(cs, prefix_all) is in
+  int32_t prefix_len; // P
+  int32_t least_own;
+  int32_t bad;
+};
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ int32_t pair_tiles(const RowsGeom &g, int32_t y, bool &bad) {
+  const int32_t b = y / g.nqb;
+  return own_unit(g, __ldg(g.seqlens + b), y - b * g.nqb, bad).n;
+}
+
+// The plan of worker c of `workers`; run by one whole warp, every lane gets it.
+__device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int32_t workers) {
+  const int lane = threadIdx.x & 31;
+  const int32_t pairs = g.batch * g.nqb;
+  RowsPlan p;
+  bool bad = false;
+  int64_t own = 0;
+  for (int32_t y = lane; y < pairs; y += 32) own += pair_tiles(g, y, bad);
+  own = warp_sum64(own) * g.n_kv_heads;
+  p.prefix_len = 0;
+  p.least_own = 0;
+  p.prefix_all = 0;
+  if (g.prefix_len != nullptr) {
+    p.prefix_len = clamp_prefix(g, __ldg(g.prefix_len), bad);
+    int32_t least = INT32_MAX;
+    if (g.window > 0) {
+      for (int32_t b = lane; b < g.batch; b += 32) {
+        const int32_t L = __ldg(g.seqlens + b);
+        if (L > 0) least = imin32(least, imax32(0, L - g.tokens));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        least = imin32(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+    p.least_own = least == INT32_MAX ? 0 : least;
+    p.prefix_all = static_cast<int64_t>(prefix_unit(g, p.prefix_len, p.least_own).n) *
+                   g.n_kv_heads * g.npb;
+  }
+  p.bad = __any_sync(0xffffffffu, bad);
+  p.total = p.prefix_all + own;
+  p.chunk = (p.total + workers - 1) / workers;
+  p.cs = p.chunk * c < p.total ? p.chunk * c : p.total;
+  p.ce = p.cs + p.chunk < p.total ? p.cs + p.chunk : p.total;
+  // The own pair whose tiles reach past the chunk's start.
+  p.y = 0;
+  p.y_start = p.prefix_all;
+  if (p.cs > p.prefix_all) {
+    int64_t base = p.prefix_all;
+    p.y = pairs;
+    for (int32_t y0 = 0; y0 < pairs; y0 += 32) {
+      const int32_t y = y0 + lane;
+      bool dummy = false;
+      const int64_t span =
+          y < pairs ? static_cast<int64_t>(pair_tiles(g, y, dummy)) * g.n_kv_heads : 0;
+      int64_t incl = span;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      incl += base;
+      const unsigned hit = __ballot_sync(0xffffffffu, y < pairs && incl > p.cs);
+      if (hit) {
+        const int first = __ffs(hit) - 1;
+        p.y = y0 + first;
+        p.y_start = __shfl_sync(0xffffffffu, incl - span, first);
+        break;
+      }
+      base = __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  return p;
+}
+
+// One (chunk, unit) piece of work: tiles [t0, t1) of the unit.
+struct RowSegment {
+  UnitTiles u;
+  int32_t t0, t1;
+  int32_t x;       // KV head
+  int32_t b, qb;   // own: sequence and block; prefix: qb is the prefix block
+  int32_t unit;    // index among the prefix units, or among the own units
+  int32_t L;       // own: the sequence's length
+  bool prefix;
+  bool opens;      // first segment of its chunk
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.n; }
+};
+
+// Walks the segments of a chunk in order; every warp that needs them runs its own.
+struct RowSegments {
+  int64_t pos, ce, cs, prefix_all, y_start;
+  int32_t y;
+  UnitTiles pu;
+
+  __device__ __forceinline__ void init(const RowsGeom &g, const RowsPlan &p) {
+    pos = cs = p.cs;
+    ce = p.ce;
+    prefix_all = p.prefix_all;
+    y_start = p.y_start;
+    y = p.y;
+    pu = prefix_unit(g, p.prefix_len, p.least_own);
+  }
+
+  __device__ __forceinline__ bool next(const RowsGeom &g, RowSegment &s) {
+    if (pos >= ce) return false;
+    s.opens = pos == cs;
+    if (pos < prefix_all) {
+      s.prefix = true;
+      s.u = pu;
+      s.unit = static_cast<int32_t>(pos / pu.n);
+      s.x = s.unit / g.npb;
+      s.qb = s.unit - s.x * g.npb;
+      s.b = 0;
+      s.L = 0;
+      const int64_t start = static_cast<int64_t>(s.unit) * pu.n;
+      s.t0 = static_cast<int32_t>(pos - start);
+      s.t1 = static_cast<int32_t>(ce - start < pu.n ? ce - start : pu.n);
+      pos = start + s.t1;
+      return true;
+    }
+    const int32_t pairs = g.batch * g.nqb;
+    for (; y < pairs; ++y) {
+      bool dummy = false;
+      s.b = y / g.nqb;
+      s.qb = y - s.b * g.nqb;
+      s.L = __ldg(g.seqlens + s.b);
+      s.u = own_unit(g, s.L, s.qb, dummy);
+      const int64_t span = static_cast<int64_t>(s.u.n) * g.n_kv_heads;
+      if (y_start + span > pos) break;
+      y_start += span;
+    }
+    if (y >= pairs) return false;
+    s.prefix = false;
+    s.x = static_cast<int32_t>((pos - y_start) / s.u.n);
+    s.unit = y * g.n_kv_heads + s.x;
+    const int64_t start = y_start + static_cast<int64_t>(s.x) * s.u.n;
+    s.t0 = static_cast<int32_t>(pos - start);
+    s.t1 = static_cast<int32_t>(ce - start < s.u.n ? ce - start : s.u.n);
+    pos = start + s.t1;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- partials
+// Slot of a segment's partial.  With a prefix every segment leaves one: chunk c
+// touching unit u of its kind writes slot c + u (if a later chunk touches unit u',
+// then u' >= u, so no two pieces share a slot).  Without one only pieces of split
+// units do, at most two a chunk: its first segment and its last.
+GDATTN_HD int64_t partial_slot(bool prefix_call, int32_t c, int32_t unit, bool opens) {
+  return prefix_call ? static_cast<int64_t>(c) + unit
+                     : 2 * static_cast<int64_t>(c) + (opens ? 0 : 1);
+}
+
+// The slots of a unit's pieces: the first one's, then next, next + step, ...
+struct PartSlots {
+  int64_t first, next, step;
+  int32_t n;
+};
+
+// Call with a prefix: a unit of its kind that starts at tile `start` and has n > 0.
+GDATTN_HD PartSlots unit_parts(int64_t chunk, int64_t start, int32_t n, int32_t unit) {
+  const int32_t cf = static_cast<int32_t>(start / chunk);
+  const int32_t cl = static_cast<int32_t>((start + n - 1) / chunk);
+  PartSlots s;
+  s.n = cl - cf + 1;
+  s.step = 1;
+  s.first = partial_slot(true, cf, unit, false);
+  s.next = s.first + 1;
+  return s;
+}
+
+// Call without a prefix: whether the boundary behind chunk c is the first one
+// inside a unit, and that unit's pieces.  seg: the first segment of chunk c + 1
+// (there must be one), which starts at tile `cs`.
+GDATTN_HD bool cut_parts(int64_t chunk, int32_t c, int64_t cs, int32_t t0, int32_t n,
+                         PartSlots &s) {
+  if (t0 == 0 || t0 > chunk) return false;  // cut by an earlier boundary, or not at all
+  const int64_t start = cs - t0;
+  s.n = static_cast<int32_t>((start + n - 1) / chunk) - c + 1;
+  s.first = partial_slot(false, c, 0, start == chunk * c);
+  s.next = partial_slot(false, c + 1, 0, true);
+  s.step = 2;
+  return true;
+}
+
+}  // namespace gdattn

@@ -81,4 +81,83 @@ GDATTN_HD int32_t oldest_in_ring(const RowsGeom &g, int32_t L) {
   return L - (g.capacity - g.sinks);
 }
 
+// ------------------------------------------------------------------- tiles
+// A unit is what one block of query rows of one KV head attends: a block of
+// consecutive tokens of one sequence over that sequence's cache ("own"), or a
+// block of (token, sequence) pairs of the batch over the prefix.  Its positions
+// are walked in tiles of at most kRowTile rows that sit in consecutive slots:
+// first the pinned positions in front of the main range, then the main range,
+// cut where the ring wraps.
+constexpr int32_t kRowTile = 64;
+
+struct UnitTiles {
+  int32_t pin;         // [0, pin): pinned positions below the main range
+  int32_t lo;          // the main range's first position, in slot0
+  int32_t slot0;
+  int32_t run0, run1;  // its positions before the ring's wrap and behind it
+  int32_t slot1;       // slot of the first position behind the wrap
+  int32_t npin, n0, n; // tiles of pin, tiles of run0, all tiles
+};
+
+struct RowTile {
+  int32_t pos, slot, ntok;
+};
+
+GDATTN_HD int32_t tiles_of(int32_t rows) { return (rows + kRowTile - 1) / kRowTile; }
+
+GDATTN_HD RowTile unit_tile(const UnitTiles &u, int32_t t) {
+  RowTile r;
+  if (t < u.npin) {
+    r.pos = r.slot = t * kRowTile;
+    r.ntok = imin32(kRowTile, u.pin - r.pos);
+  } else if (t < u.npin + u.n0) {
+    const int32_t off = (t - u.npin) * kRowTile;
+    r.pos = u.lo + off;
+    r.slot = u.slot0 + off;
+    r.ntok = imin32(kRowTile, u.run0 - off);
+  } else {
+    const int32_t off = (t - u.npin - u.n0) * kRowTile;
+    r.pos = u.lo + u.run0 + off;
+    r.slot = u.slot1 + off;
+    r.ntok = imin32(kRowTile, u.run1 - off);
+  }
+  return r;
+}
+
+// Tiles of block qb of a sequence of length L.  A block without any position
+// still has one tile, of no rows, so that its output rows are written.
+GDATTN_HD UnitTiles own_unit(const RowsGeom &g, int32_t L, int32_t qb, bool &bad) {
+  UnitTiles u = {0, 0, 0, 0, 0, g.sinks, 0, 0, 1};
+  if (bad_length(g, L)) bad = true;
+  const int32_t first = L - g.tokens + qb * g.qt_seq;
+  const int32_t hi = first + imin32(g.qt_seq, g.tokens - qb * g.qt_seq);
+  if (L <= 0 || hi <= 0) return u;
+  int32_t lo = g.window > 0 ? imax32(0, first + 1 - g.window) : 0;
+  const int32_t oldest = oldest_in_ring(g, L);
+  if (imax32(lo, g.sinks) < oldest) {  // positions that later ones overwrote
+    bad = true;
+    lo = imin32(oldest, hi);
+  }
+  u.pin = imin32(g.sinks, lo);
+  u.lo = lo;
+  u.slot0 = slot_of(lo, g.sinks, g.capacity);
+  u.run0 = imin32(hi - lo, g.capacity - u.slot0);
+  u.run1 = hi - lo - u.run0;
+  u.npin = tiles_of(u.pin);
+  u.n0 = tiles_of(u.run0);
+  u.n = imax32(1, u.npin + u.n0 + tiles_of(u.run1));
+  return u;
+}
+
+// Tiles of every prefix block: the positions that some sequence's tokens reach,
+// least_own being the fewest own positions in front of a query token.
+GDATTN_HD UnitTiles prefix_unit(const RowsGeom &g, int32_t P, int32_t least_own) {
+  UnitTiles u = {0, 0, 0, 0, 0, 0, 0, 0, 0};
+  const int64_t lo = g.window > 0 ? static_cast<int64_t>(P) + least_own + 1 - g.window : 0;
+  u.lo = u.slot0 = lo <= 0 ? 0 : (lo < P ? static_cast<int32_t>(lo) : P);
+  u.run0 = P - u.lo;
+  u.n0 = u.n = tiles_of(u.run0);
+  return u;
+}
+
 }  // namespace gdattn

@@ -6,13 +6,14 @@
 
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "gdattn.h"
 
 #include "../host_common.h"
 #include "cache_rows.cuh"
-#include "rows_plan.cuh"
-#include "simple_rows.cuh"
+#include "rows_attn.cuh"
+#include "rows_merge.cuh"
 
 using namespace gdattn;
 
@@ -23,28 +24,26 @@ constexpr int32_t kMaxGroup = 128;  // query heads per KV head: one block of que
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// What both attention entry points check on the host (the workspace aside).
+// What both attention entry points check of the pointers (the workspace aside).
 gdattn_status check_rows_args(const void *q, const void *k_cache, const void *v_cache,
-                              const int32_t *seqlens, int32_t batch, int32_t n_tokens,
-                              int32_t max_seqlen, const gdattn_layer_desc *desc, int32_t n_sink,
+                              const int32_t *seqlens, const gdattn_layer_desc *desc,
                               const void *out, const float *lse) {
   if (q == nullptr || k_cache == nullptr || seqlens == nullptr || out == nullptr ||
       desc == nullptr)
     return GDATTN_ERR_INVALID_ARG;
-  gdattn_status st = check_desc(desc);
+  const gdattn_status st = check_desc(desc);
   if (st != GDATTN_OK) return st;
   if ((desc->kv_shared == 1) != (v_cache == nullptr)) return GDATTN_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || (v_cache && !aligned16(v_cache)) ||
-      !aligned16(out) || !aligned4(seqlens) || !aligned4(lse))
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned4(seqlens) || !aligned4(lse))
     return GDATTN_ERR_MISALIGNED;
-  (void)batch, (void)n_tokens, (void)max_seqlen, (void)n_sink;
   return GDATTN_OK;
 }
 
-// Shape checks, shared with the workspace queries.
+// What they check of the shape, shared with the workspace queries.
 gdattn_status check_rows_shape(int32_t batch, int32_t n_tokens, int32_t max_seqlen,
                                const gdattn_layer_desc *desc, int32_t n_sink) {
-  gdattn_status st = check_desc(desc);
+  const gdattn_status st = check_desc(desc);
   if (st != GDATTN_OK) return st;
   if (batch <= 0 || max_seqlen <= 0 || n_tokens < 1 || n_tokens > kMaxRowsTokens ||
       n_tokens > max_seqlen || n_sink < 0 || n_sink >= desc->cache_capacity)
@@ -62,43 +61,181 @@ gdattn_status check_rows_shape(int32_t batch, int32_t n_tokens, int32_t max_seql
   return GDATTN_OK;
 }
 
-gdattn_status enqueue_rows(const void *q, const void *k_prefix, const void *v_prefix,
-                           const int32_t *prefix_len, int32_t prefix_rows, const void *k_cache,
-                           const void *v_cache, const int32_t *seqlens, int32_t batch,
-                           int32_t n_tokens, const gdattn_layer_desc *desc, int32_t n_sink,
-                           void *out, float *lse, void *workspace, cudaStream_t stream) {
-  const float log2e = 1.4426950408889634f;
-  SimpleRowsParams p = {};
-  p.g.seqlens = seqlens;
-  p.g.prefix_len = prefix_len;
-  p.g.batch = batch;
-  p.g.tokens = n_tokens;
-  p.g.n_kv_heads = desc->n_kv_heads;
-  p.g.group = desc->n_q_heads / desc->n_kv_heads;
-  p.g.window = desc->window;
-  p.g.sinks = n_sink;
-  p.g.capacity = desc->cache_capacity;
-  p.g.prefix_rows = prefix_rows;
-  p.q = static_cast<const uint16_t *>(q);
-  p.k = static_cast<const uint16_t *>(k_cache);
-  p.v = static_cast<const uint16_t *>(v_cache ? v_cache : k_cache);
-  p.pk = static_cast<const uint16_t *>(k_prefix);
-  p.pv = static_cast<const uint16_t *>(v_prefix ? v_prefix : k_prefix);
-  p.batch_stride = desc->cache_batch_stride != 0 ? desc->cache_batch_stride
-                                                 : static_cast<int64_t>(desc->cache_capacity) *
-                                                       desc->n_kv_heads * desc->head_dim;
+// ------------------------------------------------------------- row kernels
+using RowsFn = void (*)(RowsMaps, RowsParams);
+
+RowsFn rows_kernel(const gdattn_layer_desc *d) {
+  if (d->head_dim == 256)
+    return d->kv_shared ? rows_attn_kernel<1, true> : rows_attn_kernel<1, false>;
+  return d->kv_shared ? rows_attn_kernel<2, true> : rows_attn_kernel<2, false>;
+}
+
+cudaLaunchConfig_t rows_launch(int nh, int workers, cudaStream_t stream,
+                               cudaLaunchAttribute (&attr)[2]) {
+  const int smem = nh == 1 ? RowsConfig<1>::SMEM : RowsConfig<2>::SMEM;
+  cudaLaunchConfig_t cfg =
+      launch_config(dim3(static_cast<unsigned>(workers * nh)), RowsConfig<1>::kThreads, smem,
+                    stream, attr);
+  if (nh == 2) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cfg;
+}
+
+// CTAs (or CTA pairs) of the geometry's kernel that the current device holds at
+// once; also sets the kernel's shared-memory limit there.  Found once per device.
+int max_workers(const gdattn_layer_desc *d) {
+  constexpr int kDevices = 64;
+  static std::mutex mu;
+  static int known[kDevices][4] = {};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  const int nh = d->head_dim / 256;
+  int &n = known[dev][(nh - 1) * 2 + d->kv_shared];
+  std::lock_guard<std::mutex> lock(mu);
+  if (n > 0) return n;
+  const void *fn = reinterpret_cast<const void *>(rows_kernel(d));
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           nh == 1 ? RowsConfig<1>::SMEM : RowsConfig<2>::SMEM) != cudaSuccess)
+    return 0;
+  int got = 0;
+  if (nh == 1) {
+    got = sm_count();
+  } else {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = rows_launch(nh, sm_count() / 2, nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&got, fn, &cfg) != cudaSuccess) return 0;
+  }
+  return n = got;
+}
+
+struct RowsLayout {
+  RowsGeom g = {};
+  int nh = 1, workers = 0;
+  int32_t rs = 0, rp = 0;
+  size_t own_o = 0, own_lse = 0, pre_o = 0, pre_lse = 0, bytes = 0;
+};
+
+// Blocks, workers and workspace of a call (prefix_rows 0: a call without a prefix).
+gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_desc *d,
+                          int32_t n_sink, int32_t prefix_rows, RowsLayout &lay) {
+  const int most = max_workers(d);
+  if (most <= 0) return GDATTN_ERR_CUDA;
+  lay.nh = d->head_dim / 256;
+  lay.workers = d->split_ctas > 0 && d->split_ctas < most ? d->split_ctas : most;
+  RowsGeom &g = lay.g;
+  g.batch = batch;
+  g.tokens = n_tokens;
+  g.n_kv_heads = d->n_kv_heads;
+  g.group = d->n_q_heads / d->n_kv_heads;
+  g.window = d->window;
+  g.sinks = n_sink;
+  g.capacity = d->cache_capacity;
+  g.prefix_rows = prefix_rows;
+  const int32_t per_block = RowsConfig<1>::M / g.group;  // tokens of a full block
+  g.qt_seq = n_tokens < per_block ? n_tokens : per_block;
+  g.nqb = (n_tokens + g.qt_seq - 1) / g.qt_seq;
+  const int32_t pairs = batch * n_tokens;
+  g.qt_pre = pairs < per_block ? pairs : per_block;
+  g.npb = (pairs + g.qt_pre - 1) / g.qt_pre;
+  lay.rs = g.qt_seq * g.group;
+  lay.rp = g.qt_pre * g.group;
+  const int64_t own_units = static_cast<int64_t>(batch) * g.nqb * g.n_kv_heads;
+  const int64_t own_slots = prefix_rows > 0 ? lay.workers + own_units : 2 * lay.workers;
+  const int64_t pre_slots =
+      prefix_rows > 0 ? lay.workers + static_cast<int64_t>(g.npb) * g.n_kv_heads : 0;
+  const size_t own_rows = static_cast<size_t>(own_slots) * lay.rs;
+  const size_t pre_rows = static_cast<size_t>(pre_slots) * lay.rp;
+  lay.own_lse = kHeaderBytes;
+  lay.pre_lse = align256(lay.own_lse + own_rows * 4);
+  lay.own_o = align256(lay.pre_lse + pre_rows * 4);
+  lay.pre_o = align256(lay.own_o + own_rows * d->head_dim * 4);
+  lay.bytes = align256(lay.pre_o + pre_rows * d->head_dim * 4);
+  return GDATTN_OK;
+}
+
+template <int D>
+cudaError_t launch_merge(const RowsLayout &lay, const RowsParams &p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  constexpr int kRows = kMergeThreads / 32;
+  if (lay.g.prefix_len != nullptr) {
+    const int64_t rows =
+        static_cast<int64_t>(lay.g.batch) * lay.g.tokens * lay.g.n_kv_heads * lay.g.group;
+    cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),
+                                           kMergeThreads, 0, stream, attr);
+    return cudaLaunchKernelEx(&cfg, merge_prefix_kernel<D>, p);
+  }
+  if (lay.workers == 1) return cudaSuccess;  // no boundary
+  cudaLaunchConfig_t cfg =
+      launch_config(dim3(static_cast<unsigned>(lay.workers - 1),
+                         static_cast<unsigned>((lay.rs + kRows - 1) / kRows)),
+                    kMergeThreads, 0, stream, attr);
+  return cudaLaunchKernelEx(&cfg, merge_cut_units_kernel<D>, p);
+}
+
+gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
+                           const void *v_prefix, const int32_t *prefix_len, const void *k_cache,
+                           const void *v_cache, const int32_t *seqlens,
+                           const gdattn_layer_desc *desc, void *out, float *lse, uint8_t *ws,
+                           cudaStream_t stream) {
+  RowsGeom &g = lay.g;
+  g.seqlens = seqlens;
+  g.prefix_len = prefix_len;
+  const int32_t D = desc->head_dim, Hkv = desc->n_kv_heads, Hq = desc->n_q_heads;
+  const int64_t bstride = desc->cache_batch_stride != 0
+                              ? desc->cache_batch_stride
+                              : static_cast<int64_t>(desc->cache_capacity) * Hkv * D;
+  EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return GDATTN_ERR_CUDA;
+  RowsMaps m = {};
+  bool ok = true;
+  auto cache = [&](CUtensorMap *full, CUtensorMap *part, const void *base, int32_t rows,
+                   int32_t batch, int64_t stride) {
+    if (base == nullptr) return;
+    ok = ok && encode_cache_map(enc, full, base, D, Hkv, rows, batch, stride, kRowTile) &&
+         encode_cache_map(enc, part, base, D, Hkv, rows, batch, stride, 16);
+  };
+  cache(&m.k, &m.k16, k_cache, g.capacity, g.batch, bstride);
+  cache(&m.v, &m.v16, v_cache, g.capacity, g.batch, bstride);
+  const int64_t pstride = static_cast<int64_t>(g.prefix_rows) * Hkv * D;
+  cache(&m.pk, &m.pk16, k_prefix, g.prefix_rows, 1, pstride);
+  cache(&m.pv, &m.pv16, v_prefix, g.prefix_rows, 1, pstride);
+  ok = ok && encode_q_tokens_map(enc, &m.q_own, q, D, static_cast<int64_t>(g.batch) * Hq,
+                                 g.tokens, g.qt_seq, g.group);
+  if (prefix_len != nullptr)
+    ok = ok && encode_q_tokens_map(enc, &m.q_pre, q, D, Hq, g.tokens * g.batch, g.qt_pre, g.group);
+  if (!ok) return GDATTN_ERR_CUDA;
+  RowsParams p = {};
+  p.g = g;
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
-  p.status = static_cast<uint32_t *>(workspace);
+  p.own_o = reinterpret_cast<float *>(ws + lay.own_o);
+  p.own_lse = reinterpret_cast<float *>(ws + lay.own_lse);
+  p.pre_o = reinterpret_cast<float *>(ws + lay.pre_o);
+  p.pre_lse = reinterpret_cast<float *>(ws + lay.pre_lse);
+  p.status = reinterpret_cast<uint32_t *>(ws);
+  p.workers = lay.workers;
+  p.rs = lay.rs;
+  p.rp = lay.rp;
+  const int32_t rows = prefix_len != nullptr && lay.rp > lay.rs ? lay.rp : lay.rs;
+  p.q_stride = (rows + 7) / 8 * 1024;
+  p.q_bufs = 2 * 4 * p.q_stride <= RowsConfig<1>::QB ? 2 : 1;
+  p.q_bytes_own = lay.rs * 128;
+  p.q_bytes_pre = lay.rp * 128;
+  const float log2e = 1.4426950408889634f;
   p.qscale = desc->softcap > 0.f ? desc->scale / desc->softcap : desc->scale * log2e;
   p.post = desc->softcap > 0.f ? desc->softcap * log2e : 0.f;
-  if (desc->n_q_heads > 65535) return GDATTN_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(batch) * n_tokens, desc->n_q_heads);
-  if (desc->head_dim == 256)
-    simple_rows_kernel<256><<<grid, 32 * kSimpleWarps, 0, stream>>>(p);
-  else
-    simple_rows_kernel<512><<<grid, 32 * kSimpleWarps, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? GDATTN_OK : GDATTN_ERR_CUDA;
+  p.test_withhold = (desc->flags & GDATTN_FLAG_TEST_WITHHOLD_KV) ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = rows_launch(lay.nh, lay.workers, stream, attr);
+  if (cudaLaunchKernelEx(&cfg, rows_kernel(desc), m, p) != cudaSuccess) return GDATTN_ERR_CUDA;
+  const cudaError_t e =
+      lay.nh == 1 ? launch_merge<256>(lay, p, stream) : launch_merge<512>(lay, p, stream);
+  return e == cudaSuccess ? GDATTN_OK : GDATTN_ERR_CUDA;
 }
 
 gdattn_status check_write_args(const void *k_rows, const void *v_rows, int64_t row_stride,
@@ -162,7 +299,8 @@ size_t gdattn_sink_workspace_size(int32_t batch, int32_t n_tokens, int32_t max_s
   if (check_rows_shape(batch, n_tokens, max_seqlen, desc, n_sink) != GDATTN_OK ||
       desc->window == 0)
     return 0;
-  return kHeaderBytes;
+  RowsLayout lay;
+  return plan_layout(batch, n_tokens, desc, n_sink, 0, lay) == GDATTN_OK ? lay.bytes : 0;
 }
 
 gdattn_status gdattn_decode_sink(const void *q, const void *k_cache, const void *v_cache,
@@ -170,24 +308,27 @@ gdattn_status gdattn_decode_sink(const void *q, const void *k_cache, const void 
                                  int32_t max_seqlen, const gdattn_layer_desc *desc,
                                  int32_t n_sink, void *out, float *lse, void *workspace,
                                  size_t workspace_bytes, void *stream) {
-  gdattn_status st = check_rows_args(q, k_cache, v_cache, seqlens, batch, n_tokens, max_seqlen,
-                                     desc, n_sink, out, lse);
+  gdattn_status st = check_rows_args(q, k_cache, v_cache, seqlens, desc, out, lse);
   if (st != GDATTN_OK) return st;
   st = check_rows_shape(batch, n_tokens, max_seqlen, desc, n_sink);
   if (st != GDATTN_OK) return st;
   if (desc->window == 0) return GDATTN_ERR_INVALID_ARG;
   if (workspace == nullptr) return GDATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GDATTN_ERR_MISALIGNED;
-  if (workspace_bytes < kHeaderBytes) return GDATTN_ERR_WORKSPACE;
-  return enqueue_rows(q, nullptr, nullptr, nullptr, 0, k_cache, v_cache, seqlens, batch, n_tokens,
-                      desc, n_sink, out, lse, workspace, static_cast<cudaStream_t>(stream));
+  RowsLayout lay;
+  st = plan_layout(batch, n_tokens, desc, n_sink, 0, lay);
+  if (st != GDATTN_OK) return st;
+  if (workspace_bytes < lay.bytes) return GDATTN_ERR_WORKSPACE;
+  return enqueue_rows(lay, q, nullptr, nullptr, nullptr, k_cache, v_cache, seqlens, desc, out, lse,
+                      static_cast<uint8_t *>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 size_t gdattn_prefix_workspace_size(int32_t batch, int32_t n_tokens, int32_t max_seqlen,
                                     int32_t prefix_rows, const gdattn_layer_desc *desc) {
   if (check_rows_shape(batch, n_tokens, max_seqlen, desc, 0) != GDATTN_OK || prefix_rows < 1)
     return 0;
-  return kHeaderBytes;
+  RowsLayout lay;
+  return plan_layout(batch, n_tokens, desc, 0, prefix_rows, lay) == GDATTN_OK ? lay.bytes : 0;
 }
 
 gdattn_status gdattn_decode_prefix(const void *q, const void *k_prefix, const void *v_prefix,
@@ -199,8 +340,7 @@ gdattn_status gdattn_decode_prefix(const void *q, const void *k_prefix, const vo
                                    void *stream) {
   if (k_prefix == nullptr || prefix_len == nullptr || prefix_rows < 1)
     return GDATTN_ERR_INVALID_ARG;
-  gdattn_status st = check_rows_args(q, k_cache, v_cache, seqlens, batch, n_tokens, max_seqlen,
-                                     desc, 0, out, lse);
+  gdattn_status st = check_rows_args(q, k_cache, v_cache, seqlens, desc, out, lse);
   if (st != GDATTN_OK) return st;
   if ((desc->kv_shared == 1) != (v_prefix == nullptr)) return GDATTN_ERR_INVALID_ARG;
   st = check_rows_shape(batch, n_tokens, max_seqlen, desc, 0);
@@ -209,10 +349,12 @@ gdattn_status gdattn_decode_prefix(const void *q, const void *k_prefix, const vo
     return GDATTN_ERR_MISALIGNED;
   if (workspace == nullptr) return GDATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GDATTN_ERR_MISALIGNED;
-  if (workspace_bytes < kHeaderBytes) return GDATTN_ERR_WORKSPACE;
-  return enqueue_rows(q, k_prefix, v_prefix, prefix_len, prefix_rows, k_cache, v_cache, seqlens,
-                      batch, n_tokens, desc, 0, out, lse, workspace,
-                      static_cast<cudaStream_t>(stream));
+  RowsLayout lay;
+  st = plan_layout(batch, n_tokens, desc, 0, prefix_rows, lay);
+  if (st != GDATTN_OK) return st;
+  if (workspace_bytes < lay.bytes) return GDATTN_ERR_WORKSPACE;
+  return enqueue_rows(lay, q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seqlens, desc, out,
+                      lse, static_cast<uint8_t *>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 gdattn_status gdattn_slot_map(const int32_t *seqlens, const int32_t *new_lens, int32_t batch,
