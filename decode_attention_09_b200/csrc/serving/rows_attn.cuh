@@ -31,8 +31,18 @@
 // two 32 KiB score exchange buffers).  K and V tiles take turns in the ring; with
 // K = V a tile serves both products.  Partial tiles are fetched in 16-row boxes.
 //
+// TMEM: O (256 columns) and four buffers of 64 columns, each first a tile's scores,
+// then, written in place by 32 columns, its weights.
+//
 // Warps: 0 loads tiles, 3 loads Q, 1 issues Q.K and owns TMEM, 2 issues P.V, 4-7
-// run the softmax (rows 32 s .. 32 s + 31 in warp 4 + s).  Every wait is bounded.
+// and 8-11 run the softmax of even and of odd tiles.  Every wait is bounded.
+//
+// A parity wait is sound only while its barrier is in the phase waited for or the
+// next.  odone of tile j: Q.K of tile j waited for the use before it, and whoever
+// waits has seen tile j's scores; it cannot complete again before tile j + 4, which
+// needs the waiter's own weights.  refset: the two groups alternate inside a
+// segment and meet at its end.  oempty: every warp arrives behind the segment's
+// last P.V, whose first one waited for the phase before.
 #pragma once
 
 #include <cstdint>
@@ -58,12 +68,12 @@ struct RowsConfig {
   static constexpr int XB = M * TILE * 4;           // score exchange buffer: 32 KiB
   static constexpr int OFF_KV = QB;                 // Q first: its MMA reads run past short blocks
   static constexpr int OFF_X = OFF_KV + NST * TB;
-  static constexpr int OFF_BAR = OFF_X + (NH == 1 ? 0 : 2 * XB);
+  static constexpr int OFF_REF = OFF_X + (NH == 1 ? 0 : 2 * XB);  // [2][128] floats
+  static constexpr int OFF_BAR = OFF_REF + 2 * M * 4;
   static constexpr int SMEM = OFF_BAR + 1024 + 1024;
-  static constexpr int kThreads = 256;
+  static constexpr int kThreads = 384;
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t S_COL = 0;              // 2 buffers x 64
-  static constexpr uint32_t P_COL = 128;            // 2 buffers x (32 + 32)
+  static constexpr uint32_t S_COL = 0;              // 4 buffers x 64, scores then weights
   static constexpr uint32_t O_COL = 256;            // 256
 };
 static_assert(RowsConfig<1>::SMEM <= 227 * 1024 && RowsConfig<2>::SMEM <= 227 * 1024,
@@ -94,7 +104,7 @@ struct RowsMaps {
   CUtensorMap q_own, q_pre;
 };
 
-template <int NH, bool SHARED>
+template <int NH, bool SHARED, bool CAP>
 __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     rows_attn_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
   using Cfg = RowsConfig<NH>;
@@ -106,22 +116,25 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *qs = smem;
   uint8_t *kv = smem + Cfg::OFF_KV;
-  float4 *xs = reinterpret_cast<float4 *>(smem + Cfg::OFF_X);  // [2][16 column quads][128 rows]
+  // [2 groups][16 column quads][128 rows]
+  float4 *xs = reinterpret_cast<float4 *>(smem + Cfg::OFF_X);
+  float *ref = reinterpret_cast<float *>(smem + Cfg::OFF_REF);  // [2 groups][128 rows]
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
   uint64_t *full = bars;           // [5] TMA -> Q.K, P.V (and the softmax, for partial tiles)
   uint64_t *empty = bars + 5;      // [5] Q.K / P.V -> TMA
-  uint64_t *sfull = bars + 10;     // [2] Q.K -> softmax
-  uint64_t *sempty = bars + 12;    // [2] softmax -> Q.K
-  uint64_t *qfull = bars + 14;     // [2] TMA -> Q.K
-  uint64_t *qempty = bars + 16;    // [2] Q.K -> TMA
-  uint64_t *pfull = bars + 18;     // [2] softmax -> P.V
-  uint64_t *odone = bars + 20;     // [2] P.V -> softmax
-  uint64_t *drain = bars + 22;     // [2] the MMA warps: all their MMAs are done
-  uint64_t *xfull = bars + 24;     // [2][4] peer's softmax warp -> this one: its scores are here
-  uint64_t *xfree = bars + 32;     // [2][4] peer's softmax warp: read what this one sent
-  uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 40);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 41);
-  RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 42);
+  uint64_t *sfull = bars + 10;     // [4] Q.K -> softmax
+  uint64_t *pfull = bars + 14;     // [4] softmax -> P.V
+  uint64_t *odone = bars + 18;     // [4] P.V -> Q.K (the buffer is free), softmax (O is current)
+  uint64_t *qfull = bars + 22;     // [2] TMA -> Q.K
+  uint64_t *qempty = bars + 24;    // [2] Q.K -> TMA
+  uint64_t *oempty = bars + 26;    // softmax (O was read) -> P.V
+  uint64_t *drain = bars + 27;     // [2] the MMA warps: all their MMAs are done
+  uint64_t *refset = bars + 29;    // [2][4] softmax warp -> the other group's: its reference is set
+  uint64_t *xfull = bars + 37;     // [2][4] peer's softmax warp -> this one: its scores are here
+  uint64_t *xfree = bars + 45;     // [2][4] peer's softmax warp: read what this one sent
+  uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 53);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 54);
+  RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 55);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -134,16 +147,19 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&sfull[s], 1);
-      mbar_init(&sempty[s], 4);
-      mbar_init(&qfull[s], 1);
-      mbar_init(&qempty[s], 1);
       mbar_init(&pfull[s], 4);
       mbar_init(&odone[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qempty[s], 1);
       mbar_init(&drain[s], 1);
     }
+    mbar_init(oempty, 8);
     for (int s = 0; s < 8; ++s) {
+      mbar_init(&refset[s], 1);
       mbar_init(&xfull[s], 1);
       mbar_init(&xfree[s], 1);
     }
@@ -267,9 +283,9 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       const uint32_t qoff = (buf * 4 * p.q_stride) >> 4, qstep = p.q_stride >> 4;
       for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
         const uint32_t e = i * EPT;
-        const int st = e % NST, sb = i & 1;
+        const int st = e % NST, sb = i & 3;
         ok = mbar_wait(&full[st], (e / NST) & 1, abort_flag, p.status);
-        if (ok && i >= 2) ok = mbar_wait(&sempty[sb], ((i >> 1) - 1) & 1, abort_flag, p.status);
+        if (ok && i >= 4) ok = mbar_wait(&odone[sb], ((i >> 2) - 1) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -300,23 +316,27 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     // V tile as the MN-major B operand: 64-dim chunks BOXB apart, 8 rows per 1 KiB
     const uint64_t vdesc = smem_desc_sw128(smem_u32(kv), Cfg::BOXB, 1024);
     bool ok = true;
-    uint32_t i = 0;
-    while (ok && segs.next(g, seg)) {
+    uint32_t i = 0, n = 0;
+    for (; ok && segs.next(g, seg); ++n) {
       for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
         const uint32_t e = i * EPT + EPT - 1;
-        const int st = e % NST, pb = i & 1;
-        ok = mbar_wait(&pfull[pb], (i >> 1) & 1, abort_flag, p.status);
+        const int st = e % NST, pb = i & 3;
+        // The first product of a block overwrites O: its last block was read.
+        if (t == seg.t0 && n > 0) ok = mbar_wait(oempty, (n - 1) & 1, abort_flag, p.status);
+        if (ok) ok = mbar_wait(&pfull[pb], (i >> 2) & 1, abort_flag, p.status);
         if (ok) ok = mbar_wait(&full[st], (e / NST) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          // A = P from tensor memory: 16 rows' weights are 8 columns of bf16 pairs.
+          // A = P from tensor memory: 16 rows' weights are 8 columns of bf16 pairs, and
+          // each 32 columns hold the weights of 32 rows, then their remainders.
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int kk = 0; kk < TILE / 16; ++kk)
-              tc_mma_bf16_ta(tmem + Cfg::O_COL, tmem + Cfg::P_COL + pb * 64 + half * 32 + kk * 8,
+              tc_mma_bf16_ta(tmem + Cfg::O_COL,
+                             tmem + Cfg::S_COL + pb * TILE + (kk >> 1) * 32 + half * 16 + (kk & 1) * 8,
                              vdesc + ((st * Cfg::TB + kk * 2048) >> 4), idesc,
                              !(t == seg.t0 && half == 0 && kk == 0));
           tc_commit(&odone[pb]);
@@ -332,31 +352,23 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     mbar_wait(&drain[1], 0, &no_abort, p.status);
   } else {
     // --------------------------------------------------------- softmax
+    // Two groups of four warps take the tiles in turn (group i & 1 has tile i); warp
+    // qd of either owns rows 32 qd .. 32 qd + 31.  The two threads of a row agree on
+    // its reference through ref[group][row]: tile i's thread reads what tile i - 1's
+    // has set, moves it if its scores outgrew it, and sets it for tile i + 1's.
     grid_dependency_wait();  // outputs are written below
-    const int qd = warp & 3;
-    const int t128 = threadIdx.x - 128;
+    const int wg = (warp - 4) >> 2, qd = warp & 3;
+    const int t128 = threadIdx.x & 127;
     const int r = 32 * qd + lane;  // this thread's query row (TMEM lane)
     const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
     const int32_t Hq = g.n_kv_heads * g.group;
+    float *ref_own = ref + wg * Cfg::M + r, *ref_other = ref + (wg ^ 1) * Cfg::M + r;
+    uint64_t *set_own = &refset[wg * 4 + qd], *set_other = &refset[(wg ^ 1) * 4 + qd];
+    const float worst = p.qscale >= 0.f ? -INFINITY : INFINITY;  // a score nothing is below
     bool ok = true;
-    uint32_t i = 0;
-    uint32_t xi = 0;  // score exchanges so far (tiles of blocks with rows in this warp)
-    // The P.V of tile tt (and so every earlier one: they complete in order) has
-    // completed.  Each odone barrier's phases are consumed in order, and a
-    // barrier never runs two phases ahead of its waiter (the P.V two tiles on
-    // needs this warp's next P), so the parity waits cannot alias.
-    uint32_t done0 = 0, done1 = 0;  // phases consumed on odone[0], odone[1]
-    auto ensure_pv = [&](uint32_t tt) {
-      const uint32_t ph = tt >> 1;
-      if (tt & 1) {
-        for (; done1 <= ph; ++done1)
-          if (ok && !mbar_wait(&odone[1], done1 & 1, abort_flag, p.status)) ok = false;
-      } else {
-        for (; done0 <= ph; ++done0)
-          if (ok && !mbar_wait(&odone[0], done0 & 1, abort_flag, p.status)) ok = false;
-      }
-      ok = __all_sync(0xffffffffu, ok);
-    };
+    uint32_t i = 0;       // tiles so far
+    uint32_t n_own = 0;   // references this warp set
+    uint32_t n_other = 0; // references the other group's warp set, up to this tile
     while (segs.next(g, seg)) {
       // The row: its token, sequence and head, and the positions it sees.
       const int32_t qt = seg.prefix ? g.qt_pre : g.qt_seq;
@@ -379,205 +391,256 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         }
       }
       const bool act = 32 * qd < nrow;  // the warp has rows (warp-uniform)
-      float m_ref = -INFINITY, l = 0.f;
-      for (int32_t t = seg.t0; t < seg.t1; ++t) {
-        const RowTile tile = unit_tile(seg.u, t);
-        const int sb = i & 1;
-        float s[TILE];
-        if (ok && !mbar_wait(&sfull[sb], (i >> 1) & 1, abort_flag, p.status)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && act) {
-          tc_fence_after();
-          tmem_ld64(tmem + lane_base + Cfg::S_COL + sb * TILE, s);
-          tc_fence_before();
-        } else {
-#pragma unroll
-          for (int c = 0; c < TILE; ++c) s[c] = 0.f;
+      float m_ref = -INFINITY, l = 0.f;  // l: sum of this group's weights, for m_ref
+      for (int32_t t = seg.t0; t < seg.t1; ++t, ++i) {
+        const int sb = i & 3;
+        const bool mine = static_cast<int>(i & 1) == wg;
+        if (!mine && act) {
+          ++n_other;
+          continue;
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&sempty[sb]);
-        if (NH == 2 && act) {
-          // The peer holds the scores' other half of the dims: swap and add.
-          const int xb = xi & 1;
-          if (ok && xi >= 2 &&
-              !mbar_wait_cluster(&xfree[xb * 4 + qd], ((xi >> 1) - 1) & 1, abort_flag, p.status))
-            ok = false;
+        // (A warp without rows waits for the other group's tiles too: it has nothing
+        // else that keeps it from running segments ahead of the barriers' phases.)
+        if (ok) ok = mbar_wait(&sfull[sb], (i >> 2) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!mine) continue;
+        const RowTile tile = unit_tile(seg.u, t);
+        const uint32_t s_col = tmem + lane_base + Cfg::S_COL + sb * TILE;
+        if (ok && tile.ntok < TILE) {
+          // Rows behind the tile's end hold other slots, or what the ring held
+          // before (possibly NaN, which a weight of 0 would not silence): clear
+          // them.  With K = V the tile's Q.K is done: its scores are there.
+          const uint32_t e = i * EPT + EPT - 1;
+          ok = mbar_wait(&full[e % NST], (e / NST) & 1, abort_flag, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            const uint32_t dst =
-                peer_smem(smem_u32(xs + xb * (Cfg::XB / 16) + r), static_cast<uint32_t>(rank ^ 1));
+            uint8_t *vt = kv + (e % NST) * Cfg::TB;
+            const int per_box = (TILE - tile.ntok) * 8;
+#pragma unroll 1
+            for (int q = t128; q < per_box; q += 128)
 #pragma unroll
-            for (int c = 0; c < TILE / 4; ++c)
-              st_peer_v4(dst + c * (Cfg::M * 16), s[4 * c], s[4 * c + 1], s[4 * c + 2],
-                         s[4 * c + 3]);
-            __syncwarp();
-            if (lane == 0)
-              mbar_arrive_peer(peer_smem(smem_u32(&xfull[xb * 4 + qd]), rank ^ 1));
-            if (!mbar_wait_cluster(&xfull[xb * 4 + qd], (xi >> 1) & 1, abort_flag, p.status))
-              ok = false;
+              for (int box = 0; box < DH / 64; ++box)
+                *reinterpret_cast<uint4 *>(vt + box * Cfg::BOXB + (tile.ntok + (q >> 3)) * 128 +
+                                           (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();  // for the tensor core
           }
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-#pragma unroll
-            for (int c = 0; c < TILE / 4; ++c) {
-              const float4 o = xs[xb * (Cfg::XB / 16) + c * Cfg::M + r];
-              s[4 * c] += o.x;
-              s[4 * c + 1] += o.y;
-              s[4 * c + 2] += o.z;
-              s[4 * c + 3] += o.w;
-            }
-            __syncwarp();
-            if (lane == 0)
-              mbar_arrive_peer(peer_smem(smem_u32(&xfree[xb * 4 + qd]), rank ^ 1));
-          }
-          ++xi;
         }
         if (act) {
-          // Scores in log2 units (scale, then the soft-cap if there is one).
-          if (p.post != 0.f) {
-#pragma unroll
-            for (int c = 0; c < TILE; ++c) s[c] = p.post * tanhf(s[c] * p.qscale);
+          float s[TILE];
+          if (ok) {
+            tc_fence_after();
+            tmem_ld64(s_col, s);
           } else {
 #pragma unroll
-            for (int c = 0; c < TILE; ++c) s[c] *= p.qscale;
+            for (int c = 0; c < TILE; ++c) s[c] = 0.f;
+          }
+          if (NH == 2) {
+            // The peer holds the scores' other half of the dims: swap and add.
+            if (ok && n_own > 0)
+              ok = mbar_wait_cluster(&xfree[wg * 4 + qd], (n_own - 1) & 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              const uint32_t dst = peer_smem(smem_u32(xs + wg * (Cfg::XB / 16) + r), rank ^ 1);
+#pragma unroll
+              for (int c = 0; c < TILE / 4; ++c)
+                st_peer_v4(dst + c * (Cfg::M * 16), s[4 * c], s[4 * c + 1], s[4 * c + 2],
+                           s[4 * c + 3]);
+              __syncwarp();
+              if (lane == 0) mbar_arrive_peer(peer_smem(smem_u32(&xfull[wg * 4 + qd]), rank ^ 1));
+              ok = mbar_wait_cluster(&xfull[wg * 4 + qd], n_own & 1, abort_flag, p.status);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+#pragma unroll
+              for (int c = 0; c < TILE / 4; ++c) {
+                const float4 o = xs[wg * (Cfg::XB / 16) + c * Cfg::M + r];
+                s[4 * c] += o.x;
+                s[4 * c + 1] += o.y;
+                s[4 * c + 2] += o.z;
+                s[4 * c + 3] += o.w;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_peer(peer_smem(smem_u32(&xfree[wg * 4 + qd]), rank ^ 1));
+            }
           }
           // Column c is position tile.pos + c.  A tile that every row of the warp
           // sees in full needs no mask.
           const bool inside = ok && tile.ntok == TILE && tile.pos >= rg.lo &&
                               tile.pos + TILE <= rg.hi;
-          if (!__all_sync(0xffffffffu, inside)) {
+          const bool masked = !__all_sync(0xffffffffu, inside);
+          if (masked) {
             const int32_t c_lo = rg.lo - tile.pos, c_pin = rg.pin - tile.pos;
             const int32_t c_hi = ok ? imin32(rg.hi - tile.pos, tile.ntok) : 0;
 #pragma unroll
             for (int c = 0; c < TILE; ++c)
-              s[c] = ((c >= c_lo || c < c_pin) && c < c_hi) ? s[c] : -INFINITY;
+              s[c] = ((c >= c_lo || c < c_pin) && c < c_hi) ? s[c] : worst;
           }
-          float mx4[4] = {s[0], s[1], s[2], s[3]};
+          // The largest score: of the products (the scale and the soft-cap are
+          // monotonic), then scaled and capped, in log2 units.
+          float best = s[0];
+          if (p.qscale >= 0.f) {
+            float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 4; c < TILE; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          // Move the reference of a row when a score outgrew it.  The TMEM loads
-          // and stores are warp-wide: rows whose reference stays multiply by 1.
-          const bool mine = mx > m_ref + kRefStep;
-          if (__any_sync(0xffffffffu, mine)) {
-            float alpha = 1.f;
-            if (mine) {
-              alpha = m_ref == -INFINITY ? 0.f : exp2f(m_ref - mx);
-              l *= alpha;
-              m_ref = mx;
-            }
-            if (t > seg.t0) {
-              ensure_pv(i - 1);
-              if (ok) {
-                tc_fence_after();
+            for (int c = 4; c < TILE; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+            best = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          } else {
+            float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < TILE; ++c) m4[c & 3] = fminf(m4[c & 3], s[c]);
+            best = fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
+          }
+          const float mx = best == worst ? -INFINITY : score_log2<CAP>(best, p.qscale, p.post);
+          // The row's reference, as the tile before left it.
+          float prev = -INFINITY;
+          if (t > seg.t0) {
+            if (ok) ok = mbar_wait(set_other, (n_other - 1) & 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) prev = *ref_other;
+          }
+          const bool moved = mx > prev + kRefStep;
+          if (__any_sync(0xffffffffu, moved) && t > seg.t0) {
+            // The TMEM loads and stores are warp-wide: other rows multiply by 1.
+            const float alpha = moved ? (prev == -INFINITY ? 0.f : exp2f(prev - mx)) : 1.f;
+            if (ok) ok = mbar_wait(&odone[(i - 1) & 3], ((i - 1) >> 2) & 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              tc_fence_after();
 #pragma unroll 1
-                for (int cb = 0; cb < DH / 32; ++cb) {
-                  float o[32];
-                  tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+              for (int cb = 0; cb < DH / 32; ++cb) {
+                float o[32];
+                tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
 #pragma unroll
-                  for (int q = 0; q < 32; ++q) o[q] *= alpha;
-                  tmem_store32_wait(tmem + lane_base + Cfg::O_COL + cb * 32, o);
-                }
+                for (int q = 0; q < 32; ++q) o[q] *= alpha;
+                tmem_store32_wait(tmem + lane_base + Cfg::O_COL + cb * 32, o);
               }
             }
+          }
+          const float now = moved ? mx : prev;
+          *ref_own = now;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(set_own);
+          ++n_own;
+          if (now != m_ref) {
+            l = m_ref == -INFINITY ? 0.f : l * exp2f(m_ref - now);
+            m_ref = now;
           }
           // Weights: bf16 pairs (column j holds rows 2j, 2j + 1) and remainders, both
           // truncated (the upper halves of the fp32 bits; the remainder is exact in
           // fp32 before its own truncation): 2^-14 relative.  A row without any score
-          // yet (reference -inf) has only masked columns here: 2^-inf = 0.
-          const float mr = m_ref == -INFINITY ? 0.f : m_ref;
+          // yet (reference -inf) has only masked columns here.
+          const float mr = now == -INFINITY ? 0.f : now;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
-          float wh[TILE / 2], wl[TILE / 2];
 #pragma unroll
-          for (int j = 0; j < TILE / 2; ++j) {
-            const float pa = ex2_approx(s[2 * j] - mr);
-            const float pb = ex2_approx(s[2 * j + 1] - mr);
-            l4[j & 3] += pa + pb;
-            const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
-            const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
-            const float rb = pb - __uint_as_float(ub & 0xFFFF0000u);
-            wh[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
-            wl[j] = __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
+          for (int half = 0; half < 2; ++half) {
+            float w[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float sa = s[32 * half + 2 * j], sc = s[32 * half + 2 * j + 1];
+              float pa, pb;
+              if (CAP) {
+                pa = ex2_approx(score_log2<CAP>(sa, p.qscale, p.post) - mr);
+                pb = ex2_approx(score_log2<CAP>(sc, p.qscale, p.post) - mr);
+                if (masked) {  // the cap bounds a masked score too
+                  if (sa == worst) pa = 0.f;
+                  if (sc == worst) pb = 0.f;
+                }
+              } else {
+                pa = ex2_approx(fmaf(sa, p.qscale, -mr));
+                pb = ex2_approx(fmaf(sc, p.qscale, -mr));
+              }
+              l4[j & 3] += pa + pb;
+              const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
+              const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
+              const float rb = pb - __uint_as_float(ub & 0xFFFF0000u);
+              w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
+              w[16 + j] =
+                  __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
+            }
+            if (ok) tmem_store32_wait(s_col + 32 * half, w);
           }
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          if (i >= 2) ensure_pv(i - 2);  // the P.V of tile i - 2 read this P buffer
-          if (ok) {
-            tmem_store32_wait(tmem + lane_base + Cfg::P_COL + sb * 64, wh);
-            tmem_store32_wait(tmem + lane_base + Cfg::P_COL + sb * 64 + 32, wl);
-          }
-        } else if (i >= 2) {
-          ensure_pv(i - 2);  // keeps this warp's arrivals in the barrier's phase
         }
-        if (ok && tile.ntok < TILE) {
-          // Rows behind the tile's end hold other slots, or what the ring held
-          // before (possibly NaN, which a weight of 0 would not silence): clear
-          // them.  With K = V the tile's Q.K is done: its S was read.
-          const uint32_t e = i * EPT + EPT - 1;
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&full[e % NST], (e / NST) & 1, abort_flag, p.status));
-          if (ok) {
-            uint8_t *vt = kv + (e % NST) * Cfg::TB;
-            const int per_box = (TILE - tile.ntok) * 8;
-#pragma unroll 1
-            for (int box = 0; box < DH / 64; ++box)
-              for (int q = t128; q < per_box; q += 128)
-                *reinterpret_cast<uint4 *>(vt + box * Cfg::BOXB + (tile.ntok + (q >> 3)) * 128 +
-                                           (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        fence_proxy_async_smem();  // the cleared rows, for the tensor core
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&pfull[sb]);
-        ++i;
       }
-      // --- the rows' output: final, or a partial of its unit.
-      ensure_pv(i - 1);
-      if (!act) continue;
-      const bool have_o = ok;  // warp-uniform
-      const float inv = (have_o && l > 0.f) ? __fdividef(1.f, l) : 0.f;
-      const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
-      const bool final_rows = g.prefix_len == nullptr && seg.whole();
-      const int64_t orow =
-          (static_cast<int64_t>(tok) * g.batch + b) * Hq + seg.x * g.group + h;
-      const int64_t prow =
-          partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens) *
-              (seg.prefix ? p.rp : p.rs) + r;
-      uint16_t *dst = p.out + orow * Cfg::D + rank * DH;
-      float *part = (seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D + rank * DH;
-      if (have_o) tc_fence_after();
+      // --- the rows' output: final, or a partial of its unit.  The group of the
+      // last tile has the final reference; the sums are joined over ref[].
+      const bool have_last = static_cast<int>((i - 1) & 1) == wg;
+      if (act) {
+        if (!have_last) {
+          // (n_other counts the last tile's)
+          if (ok) ok = mbar_wait(set_other, (n_other - 1) & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          const float last = ok ? *ref_other : m_ref;
+          *ref_own = m_ref == -INFINITY ? 0.f : l * exp2f(m_ref - last);
+          m_ref = last;
+        }
+        pair_sync(1 + qd);
+        if (have_last) {
+          l += *ref_other;
+          *ref_own = l;
+        }
+        pair_sync(1 + qd);
+        if (!have_last) l = *ref_other;
+      }
+      if (ok) ok = mbar_wait(&odone[(i - 1) & 3], ((i - 1) >> 2) & 1, abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (act) {
+        const float inv = (ok && l > 0.f) ? __fdividef(1.f, l) : 0.f;
+        const bool final_rows = g.prefix_len == nullptr && seg.whole();
+        const int64_t orow =
+            (static_cast<int64_t>(tok) * g.batch + b) * Hq + seg.x * g.group + h;
+        const int64_t prow =
+            partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens) *
+                (seg.prefix ? p.rp : p.rs) + r;
+        // Each group writes half of the dims.
+        const int d0 = wg * (DH / 2);
+        uint16_t *dst = p.out + orow * Cfg::D + rank * DH + d0;
+        float *part = (seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D + rank * DH + d0;
+        if (ok) tc_fence_after();
 #pragma unroll 1
-      for (int cb = 0; cb < DH / 32; ++cb) {
-        float o[32];
-        if (have_o) {
-          tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
-        } else {
+        for (int cb = 0; cb < DH / 64; ++cb) {
+          float o[32];
+          if (ok) {
+            tmem_load32(tmem + lane_base + Cfg::O_COL + d0 + cb * 32, o);
+          } else {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = 0.f;
-        }
-        if (row_ok && final_rows) {
-#pragma unroll
-          for (int q = 0; q < 32; q += 8) {
-            uint4 pk;
-            pk.x = pack_bf16x2(o[q] * inv, o[q + 1] * inv);
-            pk.y = pack_bf16x2(o[q + 2] * inv, o[q + 3] * inv);
-            pk.z = pack_bf16x2(o[q + 4] * inv, o[q + 5] * inv);
-            pk.w = pack_bf16x2(o[q + 6] * inv, o[q + 7] * inv);
-            *reinterpret_cast<uint4 *>(dst + cb * 32 + q) = pk;
+            for (int q = 0; q < 32; ++q) o[q] = 0.f;
           }
-        } else if (row_ok) {
+          if (cb + 1 == DH / 64) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(oempty);
+          }
+          if (row_ok && final_rows) {
 #pragma unroll
-          for (int q = 0; q < 32; q += 4)
-            *reinterpret_cast<float4 *>(part + cb * 32 + q) =
-                make_float4(o[q] * inv, o[q + 1] * inv, o[q + 2] * inv, o[q + 3] * inv);
+            for (int q = 0; q < 32; q += 16) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                pk[k] = pack_bf16x2(o[q + 2 * k] * inv, o[q + 2 * k + 1] * inv);
+              st_global_v8(dst + cb * 32 + q, pk);
+            }
+          } else if (row_ok) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 8) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) pk[k] = __float_as_uint(o[q + k] * inv);
+              st_global_v8(part + cb * 32 + q, pk);
+            }
+          }
         }
-      }
-      tc_fence_before();
-      if (row_ok && rank == 0) {
-        if (!final_rows)
-          (seg.prefix ? p.pre_lse : p.own_lse)[prow] = lse2;
-        else if (p.lse != nullptr)
-          p.lse[orow] = l > 0.f ? lse2 * kLn2 : -INFINITY;
+        if (row_ok && rank == 0 && have_last) {
+          const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
+          if (!final_rows)
+            (seg.prefix ? p.pre_lse : p.own_lse)[prow] = lse2;
+          else if (p.lse != nullptr)
+            p.lse[orow] = l > 0.f ? lse2 * kLn2 : -INFINITY;
+        }
+      } else if (lane == 0) {
+        mbar_arrive(oempty);
       }
     }
   }

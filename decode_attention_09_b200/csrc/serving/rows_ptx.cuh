@@ -60,6 +60,28 @@ __device__ __forceinline__ void tmem_store32_wait(uint32_t taddr, const float (&
       : "memory");
 }
 
+// 32 bytes to global memory (32-byte aligned): one sector per lane.
+__device__ __forceinline__ void st_global_v8(void *dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// The two warps that share rows (64 threads), on named barrier `id`.
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+// A score in log2 units from its dot product: scaled, or scaled, capped and scaled
+// again.  tanh x = 1 - 2 / (e^2x + 1): absolute error a few 2^-24, and only the
+// absolute error of a score matters to its weight.
+template <bool CAP>
+__device__ __forceinline__ float score_log2(float s, float qscale, float post) {
+  if (!CAP) return s * qscale;
+  const float e = ex2_approx(s * (qscale * 2.8853900817779268f));  // 2 log2(e)
+  return fmaf(__fdividef(-2.f, e + 1.f), post, post);
+}
+
 // --------------------------------------------- distributed shared memory
 // All threads of the cluster's CTAs; orders their earlier shared-memory accesses.
 __device__ __forceinline__ void cluster_sync() {

@@ -65,9 +65,12 @@ gdattn_status check_rows_shape(int32_t batch, int32_t n_tokens, int32_t max_seql
 using RowsFn = void (*)(RowsMaps, RowsParams);
 
 RowsFn rows_kernel(const gdattn_layer_desc *d) {
-  if (d->head_dim == 256)
-    return d->kv_shared ? rows_attn_kernel<1, true> : rows_attn_kernel<1, false>;
-  return d->kv_shared ? rows_attn_kernel<2, true> : rows_attn_kernel<2, false>;
+  static const RowsFn fns[2][2][2] = {
+      {{rows_attn_kernel<1, false, false>, rows_attn_kernel<1, false, true>},
+       {rows_attn_kernel<1, true, false>, rows_attn_kernel<1, true, true>}},
+      {{rows_attn_kernel<2, false, false>, rows_attn_kernel<2, false, true>},
+       {rows_attn_kernel<2, true, false>, rows_attn_kernel<2, true, true>}}};
+  return fns[d->head_dim / 256 - 1][d->kv_shared][d->softcap > 0.f ? 1 : 0];
 }
 
 cudaLaunchConfig_t rows_launch(int nh, int workers, cudaStream_t stream,
@@ -91,11 +94,11 @@ cudaLaunchConfig_t rows_launch(int nh, int workers, cudaStream_t stream,
 int max_workers(const gdattn_layer_desc *d) {
   constexpr int kDevices = 64;
   static std::mutex mu;
-  static int known[kDevices][4] = {};
+  static int known[kDevices][2][2][2] = {};
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
   const int nh = d->head_dim / 256;
-  int &n = known[dev][(nh - 1) * 2 + d->kv_shared];
+  int &n = known[dev][nh - 1][d->kv_shared][d->softcap > 0.f ? 1 : 0];
   std::lock_guard<std::mutex> lock(mu);
   if (n > 0) return n;
   const void *fn = reinterpret_cast<const void *>(rows_kernel(d));
@@ -228,6 +231,9 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   p.q_bytes_pre = lay.rp * 128;
   const float log2e = 1.4426950408889634f;
   p.qscale = desc->softcap > 0.f ? desc->scale / desc->softcap : desc->scale * log2e;
+  // The kernel multiplies the infinity of a masked score by it, so it may not be 0;
+  // with a scale this small every weight still rounds to 1.
+  if (std::fabs(p.qscale) < 1e-30f) p.qscale = 1e-30f;
   p.post = desc->softcap > 0.f ? desc->softcap * log2e : 0.f;
   p.test_withhold = (desc->flags & GDATTN_FLAG_TEST_WITHHOLD_KV) ? 1 : 0;
   cudaLaunchAttribute attr[2];
