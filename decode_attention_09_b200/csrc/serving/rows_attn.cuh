@@ -9,10 +9,11 @@
 //   O[128 x D]   += P_hi[128 x 64] . V_tile[64 x D] + P_lo[128 x 64] . V_tile[64 x D]
 //
 // with the running maximum and sum of a softmax in one pass.  Every TMEM lane is a
-// query row, so a softmax thread owns a row and needs no exchange with others.
-// Weights are stored as bf16 plus the bf16 remainder (truncated; 2^-14 relative).
-// A row's reference maximum moves only when a score exceeds it by 2^8; the thread
-// then rescales its O row in TMEM.
+// query row, so a softmax thread owns a row.  Weights are stored as bf16 plus the
+// bf16 remainder (truncated; 2^-14 relative).  A row's reference moves only when a
+// score exceeds it by 2^24: floating point keeps weights above 1 as exact as those
+// below, and 2^24 times 2^17 keys times the largest |V| of a model stays far from
+// the largest fp32.  The thread then rescales its O row in TMEM.
 //
 // head_dim 512 (NH = 2): O alone would fill tensor memory, so a block runs on a
 // cluster of two CTAs, each with 256 of the dims of Q, K, V and O.  Each computes
@@ -38,7 +39,7 @@
 // and 8-11 run the softmax of even and of odd tiles.  Every wait is bounded.
 //
 // A parity wait is sound only while its barrier is in the phase waited for or the
-// next.  odone of tile j: Q.K of tile j waited for the use before it, and whoever
+// next.  kfull, vfull: their eight uses back tile i - 8's products are done.  odone of tile j: Q.K of tile j waited for the use before it, and whoever
 // waits has seen tile j's scores; it cannot complete again before tile j + 4, which
 // needs the waiter's own weights.  refset: the two groups alternate inside a
 // segment and meet at its end.  oempty: every warp arrives behind the segment's
@@ -64,6 +65,7 @@ struct RowsConfig {
   static constexpr int BOXB = TILE * 128;           // 64 rows x 64 dims: 8 KiB
   static constexpr int TB = BOXB * (DH / 64);       // a tile: 32 KiB
   static constexpr int NST = NH == 1 ? 5 : 3;       // ring
+  static constexpr uint32_t kAhead = NH == 1 ? 2 : 1;  // K tiles in front of V tiles
   static constexpr int QB = 64 * 1024;
   static constexpr int XB = M * TILE * 4;           // score exchange buffer: 32 KiB
   static constexpr int OFF_KV = QB;                 // Q first: its MMA reads run past short blocks
@@ -104,12 +106,26 @@ struct RowsMaps {
   CUtensorMap q_own, q_pre;
 };
 
+// Ring entry of tile i's K: with separate tensors K_0 .. K_a are followed by V_0,
+// K_(a+1), V_1 and so on (a = kAhead, fewer where the chunk has fewer tiles); with
+// K = V there is one entry a tile.
+template <int NH, bool SHARED>
+__device__ __forceinline__ uint32_t k_entry(uint32_t i) {
+  constexpr uint32_t a = RowsConfig<NH>::kAhead;
+  return SHARED ? i : (i <= a ? i : 2 * i - a);
+}
+// And of its V, in a chunk of n tiles: one behind K_(i + a), or behind all K.
+template <int NH, bool SHARED>
+__device__ __forceinline__ uint32_t v_entry(uint32_t i, uint32_t n) {
+  constexpr uint32_t a = RowsConfig<NH>::kAhead;
+  return SHARED ? i : (i + a < n ? 2 * i + a + 1 : n + i);
+}
+
 template <int NH, bool SHARED, bool CAP>
 __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     rows_attn_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
   using Cfg = RowsConfig<NH>;
   constexpr int DH = Cfg::DH, NST = Cfg::NST, TILE = Cfg::TILE;
-  constexpr int EPT = SHARED ? 1 : 2;  // ring entries per tile
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -120,21 +136,22 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   float4 *xs = reinterpret_cast<float4 *>(smem + Cfg::OFF_X);
   float *ref = reinterpret_cast<float *>(smem + Cfg::OFF_REF);  // [2 groups][128 rows]
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
-  uint64_t *full = bars;           // [5] TMA -> Q.K, P.V (and the softmax, for partial tiles)
-  uint64_t *empty = bars + 5;      // [5] Q.K / P.V -> TMA
-  uint64_t *sfull = bars + 10;     // [4] Q.K -> softmax
-  uint64_t *pfull = bars + 14;     // [4] softmax -> P.V
-  uint64_t *odone = bars + 18;     // [4] P.V -> Q.K (the buffer is free), softmax (O is current)
-  uint64_t *qfull = bars + 22;     // [2] TMA -> Q.K
-  uint64_t *qempty = bars + 24;    // [2] Q.K -> TMA
-  uint64_t *oempty = bars + 26;    // softmax (O was read) -> P.V
-  uint64_t *drain = bars + 27;     // [2] the MMA warps: all their MMAs are done
-  uint64_t *refset = bars + 29;    // [2][4] softmax warp -> the other group's: its reference is set
-  uint64_t *xfull = bars + 37;     // [2][4] peer's softmax warp -> this one: its scores are here
-  uint64_t *xfree = bars + 45;     // [2][4] peer's softmax warp: read what this one sent
-  uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 53);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 54);
-  RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 55);
+  uint64_t *kfull = bars;          // [8] K of tile i & 7: TMA -> Q.K (with K = V everyone)
+  uint64_t *vfull = bars + 8;      // [8] V of tile i & 7: TMA -> P.V, softmax (partial tiles)
+  uint64_t *empty = bars + 16;     // [5] ring slot: Q.K / P.V -> TMA
+  uint64_t *sfull = bars + 21;     // [4] Q.K -> softmax
+  uint64_t *pfull = bars + 25;     // [4] softmax -> P.V
+  uint64_t *odone = bars + 29;     // [4] P.V -> Q.K (the buffer is free), softmax (O is current)
+  uint64_t *qfull = bars + 33;     // [2] TMA -> Q.K
+  uint64_t *qempty = bars + 35;    // [2] Q.K -> TMA
+  uint64_t *oempty = bars + 37;    // softmax (O was read) -> P.V
+  uint64_t *drain = bars + 38;     // [2] the MMA warps: all their MMAs are done
+  uint64_t *refset = bars + 40;    // [2][4] softmax warp -> the other group's: its reference is set
+  uint64_t *xfull = bars + 48;     // [2][4] peer's softmax warp -> this one: its scores are here
+  uint64_t *xfree = bars + 56;     // [2][4] peer's softmax warp: read what this one sent
+  uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 64);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 65);
+  RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 66);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -143,10 +160,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   const int rank = NH == 1 ? 0 : static_cast<int>(blockIdx.x) % NH;  // this CTA's dims
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
+    for (int s = 0; s < NST; ++s) mbar_init(&empty[s], 1);
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], 4);
@@ -159,6 +173,8 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     }
     mbar_init(oempty, 8);
     for (int s = 0; s < 8; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&vfull[s], 1);
       mbar_init(&refset[s], 1);
       mbar_init(&xfull[s], 1);
       mbar_init(&xfree[s], 1);
@@ -189,6 +205,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_base_smem;
   const RowsPlan plan = *plan_smem;
+  const uint32_t tiles = static_cast<uint32_t>(plan.ce - plan.cs);  // of this worker
   RowSegments segs;
   segs.init(g, plan);
   RowSegment seg;
@@ -199,46 +216,66 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     if (plan.bad && worker == 0 && rank == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
     const uint64_t pol = l2_evict_first_policy();
     bool ok = true;
-    uint32_t e = 0;  // ring entries so far
-    while (ok && segs.next(g, seg)) {
-      for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
-        const RowTile tile = unit_tile(seg.u, t);
+    uint32_t e = 0;            // ring entries so far
+    uint32_t nk = 0, nv = 0;   // tiles whose K, V were loaded
+    auto load = [&](const RowSegment &sg, int32_t t, bool is_v) {
+      const RowTile tile = unit_tile(sg.u, t);
+      const int st = e % NST;
+      if (e >= NST) ok = mbar_wait(&empty[st], ((e / NST) - 1) & 1, abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      uint64_t *bar = is_v ? &vfull[nv & 7] : &kfull[nk & 7];
+      if (!(p.test_withhold && e == 0) && elect_one()) {
+        const bool big = tile.ntok > 48;
+        const int boxes = big ? 1 : (tile.ntok + 15) / 16;
+        const CUtensorMap *map =
+            sg.prefix ? (big ? (is_v ? &maps.pv : &maps.pk) : (is_v ? &maps.pv16 : &maps.pk16))
+                      : (big ? (is_v ? &maps.v : &maps.k) : (is_v ? &maps.v16 : &maps.k16));
+        uint8_t *dst = kv + st * Cfg::TB;
+        if (boxes == 0) {
+          mbar_arrive(bar);  // a tile of no rows: nothing to load
+        } else {
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>((big ? TILE : 16 * boxes) * 2 * DH));
+          for (int q = 0; q < boxes; ++q)
 #pragma unroll
-        for (int part = 0; part < EPT; ++part) {
-          const int st = e % NST;
-          if (e >= NST) ok = mbar_wait(&empty[st], ((e / NST) - 1) & 1, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (!(p.test_withhold && e == 0) && elect_one()) {
-            const bool is_v = part == 1;
-            const bool big = tile.ntok > 48;
-            const int boxes = big ? 1 : (tile.ntok + 15) / 16;
-            const CUtensorMap *map =
-                seg.prefix ? (big ? (is_v ? &maps.pv : &maps.pk) : (is_v ? &maps.pv16 : &maps.pk16))
-                           : (big ? (is_v ? &maps.v : &maps.k) : (is_v ? &maps.v16 : &maps.k16));
-            uint8_t *dst = kv + st * Cfg::TB;
-            if (boxes == 0) {
-              mbar_arrive(&full[st]);  // a tile of no rows: nothing to load
-            } else {
-              mbar_arrive_expect_tx(&full[st],
-                                    static_cast<uint32_t>((big ? TILE : 16 * boxes) * 2 * DH));
-              for (int q = 0; q < boxes; ++q)
-#pragma unroll
-                for (int j = 0; j < DH / 64; ++j)
-                  tma_load_4d(dst + j * Cfg::BOXB + q * 2048, map, rank * DH + 64 * j, seg.x,
-                              tile.slot + 16 * q, seg.b, &full[st], pol);
-            }
-          }
-          __syncwarp();
-          ++e;
+            for (int j = 0; j < DH / 64; ++j)
+              tma_load_4d(dst + j * Cfg::BOXB + q * 2048, map, rank * DH + 64 * j, sg.x,
+                          tile.slot + 16 * q, sg.b, bar, pol);
         }
       }
+      __syncwarp();
+      ++e;
+      ++(is_v ? nv : nk);
+    };
+    if (SHARED) {
+      while (ok && segs.next(g, seg))
+        for (int32_t t = seg.t0; ok && t < seg.t1; ++t) load(seg, t, false);
+    } else {
+      // K tiles run kAhead tiles in front of V tiles: a V tile is needed only after
+      // its scores' softmax, and its slot is better used by a K tile until then.
+      RowSegments vsegs = segs;
+      RowSegment vseg = {};
+      int32_t vt = 0;
+      auto load_v = [&]() {
+        if (nv == 0 || vt == vseg.t1) {
+          vsegs.next(g, vseg);
+          vt = vseg.t0;
+        }
+        load(vseg, vt++, true);
+      };
+      while (ok && segs.next(g, seg))
+        for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
+          load(seg, t, false);
+          if (ok && nk > Cfg::kAhead) load_v();
+        }
+      while (ok && nv < nk) load_v();
     }
     // Never leave with copies in flight into shared memory.
     volatile int no_abort = 0;
-    for (uint32_t f = e > NST ? e - NST : 0; f < e; ++f)
-      if (!(p.test_withhold && f == 0))
-        mbar_wait(&full[f % NST], (f / NST) & 1, &no_abort, p.status);
+    for (uint32_t f = nk > NST ? nk - NST : 0; f < nk; ++f)
+      if (!(p.test_withhold && f == 0)) mbar_wait(&kfull[f & 7], (f >> 3) & 1, &no_abort, p.status);
+    for (uint32_t f = nv > NST ? nv - NST : 0; f < nv; ++f)
+      mbar_wait(&vfull[f & 7], (f >> 3) & 1, &no_abort, p.status);
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q loads
     grid_dependency_wait();
@@ -282,9 +319,8 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       const uint32_t qoff = (buf * 4 * p.q_stride) >> 4, qstep = p.q_stride >> 4;
       for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
-        const uint32_t e = i * EPT;
-        const int st = e % NST, sb = i & 3;
-        ok = mbar_wait(&full[st], (e / NST) & 1, abort_flag, p.status);
+        const int st = k_entry<NH, SHARED>(i) % NST, sb = i & 3;
+        ok = mbar_wait(&kfull[i & 7], (i >> 3) & 1, abort_flag, p.status);
         if (ok && i >= 4) ok = mbar_wait(&odone[sb], ((i >> 2) - 1) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -319,12 +355,11 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     uint32_t i = 0, n = 0;
     for (; ok && segs.next(g, seg); ++n) {
       for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
-        const uint32_t e = i * EPT + EPT - 1;
-        const int st = e % NST, pb = i & 3;
+        const int st = v_entry<NH, SHARED>(i, tiles) % NST, pb = i & 3;
         // The first product of a block overwrites O: its last block was read.
         if (t == seg.t0 && n > 0) ok = mbar_wait(oempty, (n - 1) & 1, abort_flag, p.status);
         if (ok) ok = mbar_wait(&pfull[pb], (i >> 2) & 1, abort_flag, p.status);
-        if (ok) ok = mbar_wait(&full[st], (e / NST) & 1, abort_flag, p.status);
+        if (ok) ok = mbar_wait(SHARED ? &kfull[i & 7] : &vfull[i & 7], (i >> 3) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -364,7 +399,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     const int32_t Hq = g.n_kv_heads * g.group;
     float *ref_own = ref + wg * Cfg::M + r, *ref_other = ref + (wg ^ 1) * Cfg::M + r;
     uint64_t *set_own = &refset[wg * 4 + qd], *set_other = &refset[(wg ^ 1) * 4 + qd];
-    const float worst = p.qscale >= 0.f ? -INFINITY : INFINITY;  // a score nothing is below
+    const float sign = p.qscale >= 0.f ? 1.f : -1.f;
     bool ok = true;
     uint32_t i = 0;       // tiles so far
     uint32_t n_own = 0;   // references this warp set
@@ -410,11 +445,11 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // Rows behind the tile's end hold other slots, or what the ring held
           // before (possibly NaN, which a weight of 0 would not silence): clear
           // them.  With K = V the tile's Q.K is done: its scores are there.
-          const uint32_t e = i * EPT + EPT - 1;
-          ok = mbar_wait(&full[e % NST], (e / NST) & 1, abort_flag, p.status);
+          const int st = v_entry<NH, SHARED>(i, tiles) % NST;
+          ok = mbar_wait(SHARED ? &kfull[i & 7] : &vfull[i & 7], (i >> 3) & 1, abort_flag, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            uint8_t *vt = kv + (e % NST) * Cfg::TB;
+            uint8_t *vt = kv + st * Cfg::TB;
             const int per_box = (TILE - tile.ntok) * 8;
 #pragma unroll 1
             for (int q = t128; q < per_box; q += 128)
@@ -426,70 +461,82 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           }
         }
         if (act) {
-          float s[TILE];
-          if (ok) {
-            tc_fence_after();
-            tmem_ld64(s_col, s);
-          } else {
-#pragma unroll
-            for (int c = 0; c < TILE; ++c) s[c] = 0.f;
-          }
+          // The tile is walked in halves of 32 columns by loops that stay rolled: the
+          // unrolled softmax of 64 columns does not fit the instruction cache beside
+          // the other warps' code, and its misses cost more than the second read of
+          // the scores from tensor memory.
+          if (ok) tc_fence_after();
           if (NH == 2) {
             // The peer holds the scores' other half of the dims: swap and add.
             if (ok && n_own > 0)
               ok = mbar_wait_cluster(&xfree[wg * 4 + qd], (n_own - 1) & 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);
+            float4 *mine_x = xs + wg * (Cfg::XB / 16) + r;
             if (ok) {
-              const uint32_t dst = peer_smem(smem_u32(xs + wg * (Cfg::XB / 16) + r), rank ^ 1);
+              const uint32_t dst = peer_smem(smem_u32(mine_x), rank ^ 1);
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                float s[32];
+                tmem_load32(s_col + 32 * half, s);
 #pragma unroll
-              for (int c = 0; c < TILE / 4; ++c)
-                st_peer_v4(dst + c * (Cfg::M * 16), s[4 * c], s[4 * c + 1], s[4 * c + 2],
-                           s[4 * c + 3]);
+                for (int c = 0; c < 8; ++c)
+                  st_peer_v4(dst + (8 * half + c) * (Cfg::M * 16), s[4 * c], s[4 * c + 1],
+                             s[4 * c + 2], s[4 * c + 3]);
+              }
               __syncwarp();
               if (lane == 0) mbar_arrive_peer(peer_smem(smem_u32(&xfull[wg * 4 + qd]), rank ^ 1));
               ok = mbar_wait_cluster(&xfull[wg * 4 + qd], n_own & 1, abort_flag, p.status);
             }
             ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
+          }
+          // Column c is position tile.pos + c; bit c of `seen` says whether the row sees
+          // it.  A tile that every row of the warp sees in full needs no mask.  (Lanes
+          // without a row may compute anything: nothing of it is stored.)
+          const bool inside = ok && tile.ntok == TILE &&
+                              (!row_ok || (tile.pos >= rg.lo && tile.pos + TILE <= rg.hi));
+          const bool masked = !__all_sync(0xffffffffu, inside);
+          uint64_t seen = ~0ull;
+          if (masked) {
+            const int32_t hi = ok ? imin32(rg.hi - tile.pos, tile.ntok) : 0;
+            seen = (~low_bits(rg.lo - tile.pos) | low_bits(rg.pin - tile.pos)) & low_bits(hi);
+          }
+          // The largest product (times the scale's sign: scale and soft-cap are monotonic).
+          float best = -INFINITY;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float s[32];
+            if (ok) tmem_load32(s_col + 32 * half, s);
+            if (NH == 2 && ok) {
+              const float4 *x = xs + wg * (Cfg::XB / 16) + half * 8 * Cfg::M + r;
 #pragma unroll
-              for (int c = 0; c < TILE / 4; ++c) {
-                const float4 o = xs[wg * (Cfg::XB / 16) + c * Cfg::M + r];
+              for (int c = 0; c < 8; ++c) {
+                const float4 o = x[c * Cfg::M];
                 s[4 * c] += o.x;
                 s[4 * c + 1] += o.y;
                 s[4 * c + 2] += o.z;
                 s[4 * c + 3] += o.w;
               }
-              __syncwarp();
-              if (lane == 0) mbar_arrive_peer(peer_smem(smem_u32(&xfree[wg * 4 + qd]), rank ^ 1));
+              tmem_store32(s_col + 32 * half, s);
             }
-          }
-          // Column c is position tile.pos + c.  A tile that every row of the warp
-          // sees in full needs no mask.
-          const bool inside = ok && tile.ntok == TILE && tile.pos >= rg.lo &&
-                              tile.pos + TILE <= rg.hi;
-          const bool masked = !__all_sync(0xffffffffu, inside);
-          if (masked) {
-            const int32_t c_lo = rg.lo - tile.pos, c_pin = rg.pin - tile.pos;
-            const int32_t c_hi = ok ? imin32(rg.hi - tile.pos, tile.ntok) : 0;
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (masked) {
+              const uint32_t bits = static_cast<uint32_t>(seen >> (32 * half));
 #pragma unroll
-            for (int c = 0; c < TILE; ++c)
-              s[c] = ((c >= c_lo || c < c_pin) && c < c_hi) ? s[c] : worst;
-          }
-          // The largest score: of the products (the scale and the soft-cap are
-          // monotonic), then scaled and capped, in log2 units.
-          float best = s[0];
-          if (p.qscale >= 0.f) {
-            float m4[4] = {s[0], s[1], s[2], s[3]};
+              for (int c = 0; c < 32; ++c)
+                m4[c & 3] = fmaxf(m4[c & 3], (bits >> c) & 1 ? s[c] * sign : -INFINITY);
+            } else {
 #pragma unroll
-            for (int c = 4; c < TILE; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-            best = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          } else {
-            float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int c = 4; c < TILE; ++c) m4[c & 3] = fminf(m4[c & 3], s[c]);
-            best = fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
+              for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
+            }
+            best = fmaxf(best, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
           }
-          const float mx = best == worst ? -INFINITY : score_log2<CAP>(best, p.qscale, p.post);
+          if (NH == 2 && ok) {
+            tmem_store_wait();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(peer_smem(smem_u32(&xfree[wg * 4 + qd]), rank ^ 1));
+          }
+          const float mx =
+              best == -INFINITY ? -INFINITY : score_log2<CAP>(best * sign, p.qscale, p.post);
           // The row's reference, as the tile before left it.
           float prev = -INFINITY;
           if (t > seg.t0) {
@@ -497,10 +544,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (ok) prev = *ref_other;
           }
-          const bool moved = mx > prev + kRefStep;
-          if (__any_sync(0xffffffffu, moved) && t > seg.t0) {
+          const bool moved = row_ok && mx > prev + kRefStep;
+          // (A row without a reference has only zeros in O.)
+          const bool rescale = moved && prev != -INFINITY;
+          if (__any_sync(0xffffffffu, rescale)) {
             // The TMEM loads and stores are warp-wide: other rows multiply by 1.
-            const float alpha = moved ? (prev == -INFINITY ? 0.f : exp2f(prev - mx)) : 1.f;
+            const float alpha = rescale ? exp2f(prev - mx) : 1.f;
             if (ok) ok = mbar_wait(&odone[(i - 1) & 3], ((i - 1) >> 2) & 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
@@ -511,8 +560,9 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
                 tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
 #pragma unroll
                 for (int q = 0; q < 32; ++q) o[q] *= alpha;
-                tmem_store32_wait(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+                tmem_store32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
               }
+              tmem_store_wait();
             }
           }
           const float now = moved ? mx : prev;
@@ -530,24 +580,22 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // yet (reference -inf) has only masked columns here.
           const float mr = now == -INFINITY ? 0.f : now;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            float w[32];
+            float s[32], w[32];
+            if (ok) tmem_load32(s_col + 32 * half, s);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              s[c] = CAP ? ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr)
+                         : ex2_approx(fmaf(s[c], p.qscale, -mr));
+            if (masked) {
+              const uint32_t bits = static_cast<uint32_t>(seen >> (32 * half));
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float sa = s[32 * half + 2 * j], sc = s[32 * half + 2 * j + 1];
-              float pa, pb;
-              if (CAP) {
-                pa = ex2_approx(score_log2<CAP>(sa, p.qscale, p.post) - mr);
-                pb = ex2_approx(score_log2<CAP>(sc, p.qscale, p.post) - mr);
-                if (masked) {  // the cap bounds a masked score too
-                  if (sa == worst) pa = 0.f;
-                  if (sc == worst) pb = 0.f;
-                }
-              } else {
-                pa = ex2_approx(fmaf(sa, p.qscale, -mr));
-                pb = ex2_approx(fmaf(sc, p.qscale, -mr));
-              }
+              const float pa = s[2 * j], pb = s[2 * j + 1];
               l4[j & 3] += pa + pb;
               const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
               const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
@@ -556,8 +604,9 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
               w[16 + j] =
                   __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
             }
-            if (ok) tmem_store32_wait(s_col + 32 * half, w);
+            if (ok) tmem_store32(s_col + 32 * half, w);
           }
+          if (ok) tmem_store_wait();
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         }
         tc_fence_before();
@@ -613,13 +662,14 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(oempty);
           }
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] *= inv;
           if (row_ok && final_rows) {
 #pragma unroll
             for (int q = 0; q < 32; q += 16) {
               uint32_t pk[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                pk[k] = pack_bf16x2(o[q + 2 * k] * inv, o[q + 2 * k + 1] * inv);
+              for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(o[q + 2 * k], o[q + 2 * k + 1]);
               st_global_v8(dst + cb * 32 + q, pk);
             }
           } else if (row_ok) {
@@ -627,7 +677,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             for (int q = 0; q < 32; q += 8) {
               uint32_t pk[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) pk[k] = __float_as_uint(o[q + k] * inv);
+              for (int k = 0; k < 8; ++k) pk[k] = __float_as_uint(o[q + k]);
               st_global_v8(part + cb * 32 + q, pk);
             }
           }

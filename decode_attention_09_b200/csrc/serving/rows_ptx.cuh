@@ -9,8 +9,8 @@
 
 namespace gdattn {
 
-// A row's reference maximum moves when a score exceeds it by 2^kRefStep.
-constexpr float kRefStep = 8.f;
+// A row's reference moves when a score exceeds it by a factor of 2^kRefStep.
+constexpr float kRefStep = 24.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // A box of query rows: 64 dims of consecutive heads of consecutive tokens.
@@ -43,21 +43,25 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tmem_store32_wait(uint32_t taddr, const float (&v)[32]) {
+// Store 32 consecutive columns; tmem_store_wait before anyone reads them.
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const float (&v)[32]) {
   uint32_t r[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-      "%29, %30, %31, %32};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "%29, %30, %31, %32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_store_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // 32 bytes to global memory (32-byte aligned): one sector per lane.
@@ -70,6 +74,11 @@ __device__ __forceinline__ void st_global_v8(void *dst, const uint32_t (&v)[8]) 
 // The two warps that share rows (64 threads), on named barrier `id`.
 __device__ __forceinline__ void pair_sync(int id) {
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+// The n lowest bits set (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ uint64_t low_bits(int32_t n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
 // A score in log2 units from its dot product: scaled, or scaled, capped and scaled

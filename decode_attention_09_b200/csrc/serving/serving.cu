@@ -231,9 +231,6 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   p.q_bytes_pre = lay.rp * 128;
   const float log2e = 1.4426950408889634f;
   p.qscale = desc->softcap > 0.f ? desc->scale / desc->softcap : desc->scale * log2e;
-  // The kernel multiplies the infinity of a masked score by it, so it may not be 0;
-  // with a scale this small every weight still rounds to 1.
-  if (std::fabs(p.qscale) < 1e-30f) p.qscale = 1e-30f;
   p.post = desc->softcap > 0.f ? desc->softcap * log2e : 0.f;
   p.test_withhold = (desc->flags & GDATTN_FLAG_TEST_WITHHOLD_KV) ? 1 : 0;
   cudaLaunchAttribute attr[2];
