@@ -33,7 +33,7 @@
 // K = V a tile serves both products.  Partial tiles are fetched in 16-row boxes.
 //
 // TMEM: O (256 columns) and four buffers of 64 columns, each first a tile's scores,
-// then, written in place by 32 columns, its weights.
+// then, written in place by 16 columns, its weights.
 //
 // Warps: 0 loads tiles, 3 loads Q, 1 issues Q.K and owns TMEM, 2 issues P.V, 4-7
 // and 8-11 run the softmax of even and of odd tiles.  Every wait is bounded.
@@ -236,8 +236,9 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           mbar_arrive(bar);  // a tile of no rows: nothing to load
         } else {
           mbar_arrive_expect_tx(bar, static_cast<uint32_t>((big ? TILE : 16 * boxes) * 2 * DH));
+#pragma unroll 1
           for (int q = 0; q < boxes; ++q)
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < DH / 64; ++j)
               tma_load_4d(dst + j * Cfg::BOXB + q * 2048, map, rank * DH + 64 * j, sg.x,
                           tile.slot + 16 * q, sg.b, bar, pol);
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       if (elect_one()) {
         uint8_t *dst = qs + buf * 4 * p.q_stride;
         mbar_arrive_expect_tx(&qfull[buf], 4 * (seg.prefix ? p.q_bytes_pre : p.q_bytes_own));
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < DH / 64; ++j) {
           if (seg.prefix)
             tma_load_tokens(dst + j * p.q_stride, &maps.q_pre, rank * DH + 64 * j, seg.x * g.group,
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < DH / 64; ++j)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -364,16 +365,15 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          // A = P from tensor memory: 16 rows' weights are 8 columns of bf16 pairs, and
-          // each 32 columns hold the weights of 32 rows, then their remainders.
+          // A = P from tensor memory: 16 rows' weights are 8 columns of bf16 pairs,
+          // followed by the 8 columns of their remainders.
+#pragma unroll 1
+          for (int kk = 0; kk < TILE / 16; ++kk)
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int kk = 0; kk < TILE / 16; ++kk)
-              tc_mma_bf16_ta(tmem + Cfg::O_COL,
-                             tmem + Cfg::S_COL + pb * TILE + (kk >> 1) * 32 + half * 16 + (kk & 1) * 8,
+            for (int part = 0; part < 2; ++part)
+              tc_mma_bf16_ta(tmem + Cfg::O_COL, tmem + Cfg::S_COL + pb * TILE + kk * 16 + part * 8,
                              vdesc + ((st * Cfg::TB + kk * 2048) >> 4), idesc,
-                             !(t == seg.t0 && half == 0 && kk == 0));
+                             !(t == seg.t0 && kk == 0 && part == 0));
           tc_commit(&odone[pb]);
           tc_commit(&empty[st]);
         }
@@ -461,10 +461,10 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           }
         }
         if (act) {
-          // The tile is walked in halves of 32 columns by loops that stay rolled: the
-          // unrolled softmax of 64 columns does not fit the instruction cache beside
-          // the other warps' code, and its misses cost more than the second read of
-          // the scores from tensor memory.
+          // The tile is walked by 16 columns in loops that stay rolled: the unrolled
+          // softmax of 64 columns does not fit the instruction cache beside the other
+          // warps' code, and its misses cost more than the second read of the scores
+          // from tensor memory.
           if (ok) tc_fence_after();
           if (NH == 2) {
             // The peer holds the scores' other half of the dims: swap and add.
@@ -475,12 +475,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             if (ok) {
               const uint32_t dst = peer_smem(smem_u32(mine_x), rank ^ 1);
 #pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
-                float s[32];
-                tmem_load32(s_col + 32 * half, s);
+              for (int ch = 0; ch < TILE / 16; ++ch) {
+                float s[16];
+                tmem_ld16(s_col + 16 * ch, s);
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  st_peer_v4(dst + (8 * half + c) * (Cfg::M * 16), s[4 * c], s[4 * c + 1],
+                for (int c = 0; c < 4; ++c)
+                  st_peer_v4(dst + (4 * ch + c) * (Cfg::M * 16), s[4 * c], s[4 * c + 1],
                              s[4 * c + 2], s[4 * c + 3]);
               }
               __syncwarp();
@@ -503,32 +503,32 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // The largest product (times the scale's sign: scale and soft-cap are monotonic).
           float best = -INFINITY;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            float s[32];
-            if (ok) tmem_load32(s_col + 32 * half, s);
+          for (int ch = 0; ch < TILE / 16; ++ch) {
+            float s[16];
+            if (ok) tmem_ld16(s_col + 16 * ch, s);
             if (NH == 2 && ok) {
-              const float4 *x = xs + wg * (Cfg::XB / 16) + half * 8 * Cfg::M + r;
+              const float4 *x = xs + wg * (Cfg::XB / 16) + ch * 4 * Cfg::M + r;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
+              for (int c = 0; c < 4; ++c) {
                 const float4 o = x[c * Cfg::M];
                 s[4 * c] += o.x;
                 s[4 * c + 1] += o.y;
                 s[4 * c + 2] += o.z;
                 s[4 * c + 3] += o.w;
               }
-              tmem_store32(s_col + 32 * half, s);
+              tmem_store16(s_col + 16 * ch, s);
             }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const uint32_t bits = static_cast<uint32_t>(seen >> (16 * ch));
+            float m4[4] = {best, best, best, best};
             if (masked) {
-              const uint32_t bits = static_cast<uint32_t>(seen >> (32 * half));
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
+              for (int c = 0; c < 16; ++c)
                 m4[c & 3] = fmaxf(m4[c & 3], (bits >> c) & 1 ? s[c] * sign : -INFINITY);
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
+              for (int c = 0; c < 16; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
             }
-            best = fmaxf(best, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+            best = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
           if (NH == 2 && ok) {
             tmem_store_wait();
@@ -555,12 +555,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
-              for (int cb = 0; cb < DH / 32; ++cb) {
-                float o[32];
-                tmem_load32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+              for (int cb = 0; cb < DH / 16; ++cb) {
+                float o[16];
+                tmem_ld16(tmem + lane_base + Cfg::O_COL + cb * 16, o);
 #pragma unroll
-                for (int q = 0; q < 32; ++q) o[q] *= alpha;
-                tmem_store32(tmem + lane_base + Cfg::O_COL + cb * 32, o);
+                for (int q = 0; q < 16; ++q) o[q] *= alpha;
+                tmem_store16(tmem + lane_base + Cfg::O_COL + cb * 16, o);
               }
               tmem_store_wait();
             }
@@ -581,30 +581,30 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           const float mr = now == -INFINITY ? 0.f : now;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            float s[32], w[32];
-            if (ok) tmem_load32(s_col + 32 * half, s);
+          for (int ch = 0; ch < TILE / 16; ++ch) {
+            float s[16], w[16];
+            if (ok) tmem_ld16(s_col + 16 * ch, s);
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
+            for (int c = 0; c < 16; ++c)
               s[c] = CAP ? ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr)
                          : ex2_approx(fmaf(s[c], p.qscale, -mr));
             if (masked) {
-              const uint32_t bits = static_cast<uint32_t>(seen >> (32 * half));
+              const uint32_t bits = static_cast<uint32_t>(seen >> (16 * ch));
 #pragma unroll
-              for (int c = 0; c < 32; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
+              for (int c = 0; c < 16; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
               const float pa = s[2 * j], pb = s[2 * j + 1];
               l4[j & 3] += pa + pb;
               const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
               const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
               const float rb = pb - __uint_as_float(ub & 0xFFFF0000u);
               w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
-              w[16 + j] =
+              w[8 + j] =
                   __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
             }
-            if (ok) tmem_store32(s_col + 32 * half, w);
+            if (ok) tmem_store16(s_col + 16 * ch, w);
           }
           if (ok) tmem_store_wait();
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
@@ -649,36 +649,30 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         float *part = (seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D + rank * DH + d0;
         if (ok) tc_fence_after();
 #pragma unroll 1
-        for (int cb = 0; cb < DH / 64; ++cb) {
-          float o[32];
+        for (int cb = 0; cb < DH / 32; ++cb) {
+          float o[16];
           if (ok) {
-            tmem_load32(tmem + lane_base + Cfg::O_COL + d0 + cb * 32, o);
+            tmem_ld16(tmem + lane_base + Cfg::O_COL + d0 + cb * 16, o);
           } else {
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] = 0.f;
+            for (int q = 0; q < 16; ++q) o[q] = 0.f;
           }
-          if (cb + 1 == DH / 64) {
+          if (cb + 1 == DH / 32) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(oempty);
           }
+          uint32_t pk[8];
+          if (final_rows) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] *= inv;
-          if (row_ok && final_rows) {
+            for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+            if (row_ok) st_global_v8(dst + cb * 16, pk);
+          } else {
 #pragma unroll
-            for (int q = 0; q < 32; q += 16) {
-              uint32_t pk[8];
+            for (int q = 0; q < 16; q += 8) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(o[q + 2 * k], o[q + 2 * k + 1]);
-              st_global_v8(dst + cb * 32 + q, pk);
-            }
-          } else if (row_ok) {
-#pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-              uint32_t pk[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) pk[k] = __float_as_uint(o[q + k]);
-              st_global_v8(part + cb * 32 + q, pk);
+              for (int k = 0; k < 8; ++k) pk[k] = __float_as_uint(o[q + k] * inv);
+              if (row_ok) st_global_v8(part + cb * 16 + q, pk);
             }
           }
         }
