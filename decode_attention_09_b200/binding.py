@@ -9,7 +9,6 @@ fallback: if the library has not been built, loading it raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -490,30 +489,69 @@ def read_probe(src: torch.Tensor, mode: int, sink: torch.Tensor, stream=None) ->
 
 
 # ------------------------------------------------------ continuous batching
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _on_device(device):
-    """Context in which ``device`` is the current one: the library launches on the
-    current device, so a call follows its tensors."""
+# These wrappers are called once per layer and step, so what they cost the host counts:
+# an argument is first tested as a whole (``_fits``), and only one that fails goes
+# through the checks that name what is wrong with it.
+def _call(fn, what: str, device, stream, *args) -> None:
+    """fn(*args, stream) with ``device`` current: the library launches on the current
+    device, so a call follows its tensors.  stream None: the device's current one."""
     index = device.index
-    if index is None or index == torch.cuda.current_device():
-        return _NO_SWITCH
-    return torch.cuda.device(device)
+    if index is not None and index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, what, device, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(-1 if index is None else index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = fn(*args, stream)
+    if st != GDATTN_OK:
+        raise GdattnError(st, what)
 
 
-def _check_tokens(q, k, v, seqlens, out, lse, desc) -> None:
+def _fits(t: torch.Tensor, dtype, numel: int, device) -> bool:
+    return (t.dtype is dtype and t.device == device and t.is_contiguous()
+            and t.numel() >= numel)
+
+
+def _need(t: torch.Tensor, name: str, dtype, numel: int, device) -> None:
+    if not _fits(t, dtype, numel, device):
+        _dense(t, name, (dtype,), numel, device)
+
+
+def _need_cache(t: torch.Tensor, name: str, dtypes, numel: int, device) -> None:
+    if not _fits(t, dtypes[0], numel, device):  # dense caches; strided ones reach further
+        _extent(t, name, dtypes, numel, device)
+
+
+def _check_tokens(q, k, v, seqlens, out, lse, desc):
     """The arguments both continuous-batching attention calls share: q and out bf16
-    [T, B, Hq, D], lse fp32 [T, B, Hq] or None, caches spanning B sequences."""
+    [T, B, Hq, D], lse fp32 [T, B, Hq] or None, caches spanning B sequences.  Returns
+    (T, B, device, out, lse), with out and lse allocated where they are None."""
     T, B, Hq, D = q.shape
+    device = q.device
     if Hq != desc.n_q_heads or D != desc.head_dim:
         raise ValueError(f"q: heads and head_dim {(Hq, D)}, the descriptor has "
                          f"{(int(desc.n_q_heads), int(desc.head_dim))}")
-    _check_layer(q, k, v, seqlens, out, lse, desc, T * B, B)
+    if q.dtype is not torch.bfloat16 or not q.is_contiguous() or not q.is_cuda:
+        _dense(q, "q", _BF16, q.numel(), device)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, T * B * Hq * D, device)
+    if lse is None:
+        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=device)
+    else:
+        _need(lse, "lse", torch.float32, T * B * Hq, device)
+    n = _cache_elems(B, desc)
+    _need_cache(k, "k", _BF16, n, device)
+    if v is not None:
+        _need_cache(v, "v", _BF16, n, device)
+    _need(seqlens, "seqlens", torch.int32, B, device)
+    return T, B, device, out, lse
 
 
 def _check_workspace(workspace, device) -> None:
-    _dense(workspace, "workspace", (torch.uint8,), 0, device)
+    _need(workspace, "workspace", torch.uint8, 0, device)
 
 
 def sink_workspace_size(batch: int, n_tokens: int, max_seqlen: int, desc: LayerDesc,
@@ -545,7 +583,8 @@ def alloc_prefix_workspace(batch: int, n_tokens: int, max_seqlen: int, prefix_ro
 
 
 def _zeroed_workspace(size, what: str, device, stream) -> torch.Tensor:
-    with _on_device(torch.device(device)):
+    device = torch.device(device)
+    with torch.cuda.device(device):
         n = size()
         if n == 0:
             raise GdattnError(GDATTN_ERR_INVALID_ARG, what)
@@ -569,22 +608,13 @@ def decode_sink(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
     """Sliding-window attention with n_sink pinned first tokens through
     gdattn_decode_sink.  q bf16 [T, B, Hq, D]: token t of sequence b at position
     L_b - T + t.  Returns (out, lse), token-major."""
-    T, B, Hq, D = q.shape
-    device = q.device
-    if out is None:
-        out = torch.empty((T, B, Hq, D), dtype=torch.bfloat16, device=device)
-    if lse is None:
-        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=device)
-    _check_tokens(q, k, v, seqlens, out, lse, desc)
+    T, B, device, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
     if workspace is None:
         workspace = alloc_sink_workspace(B, T, max_seqlen, desc, n_sink, device, stream)
     _check_workspace(workspace, device)
-    with _on_device(device):
-        st = decode_sink_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(seqlens), B, T, max_seqlen, desc,
-                             n_sink, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                             _stream_handle(stream))
-    if st != GDATTN_OK:
-        raise GdattnError(st, "gdattn_decode_sink")
+    _call(lib().gdattn_decode_sink, "gdattn_decode_sink", device, stream, q.data_ptr(),
+          k.data_ptr(), _ptr(v), seqlens.data_ptr(), B, T, max_seqlen, ctypes.byref(desc), n_sink,
+          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -608,28 +638,20 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: Optional[to
     q bf16 [T, B, Hq, D]; k_prefix / v_prefix bf16 [prefix_rows, Hkv, D] (v_prefix None
     when K = V); prefix_len int32 [1] on the device; k, v, seqlens the sequences' own
     caches and lengths.  Returns (out, lse), token-major."""
-    T, B, Hq, D = q.shape
-    device = q.device
-    if out is None:
-        out = torch.empty((T, B, Hq, D), dtype=torch.bfloat16, device=device)
-    if lse is None:
-        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=device)
-    _check_tokens(q, k, v, seqlens, out, lse, desc)
+    T, B, device, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
     rows = k_prefix.shape[0]
-    _dense(k_prefix, "k_prefix", _BF16, rows * int(desc.n_kv_heads) * D, device)
+    n = rows * desc.n_kv_heads * desc.head_dim
+    _need(k_prefix, "k_prefix", torch.bfloat16, n, device)
     if v_prefix is not None:
-        _dense(v_prefix, "v_prefix", _BF16, rows * int(desc.n_kv_heads) * D, device)
-    _dense(prefix_len, "prefix_len", _I32, 1, device)
+        _need(v_prefix, "v_prefix", torch.bfloat16, n, device)
+    _need(prefix_len, "prefix_len", torch.int32, 1, device)
     if workspace is None:
         workspace = alloc_prefix_workspace(B, T, max_seqlen, rows, desc, device, stream)
     _check_workspace(workspace, device)
-    with _on_device(device):
-        st = decode_prefix_raw(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), rows,
-                               _ptr(k), _ptr(v), _ptr(seqlens), B, T, max_seqlen, desc, _ptr(out),
-                               _ptr(lse), _ptr(workspace), workspace.numel(),
-                               _stream_handle(stream))
-    if st != GDATTN_OK:
-        raise GdattnError(st, "gdattn_decode_prefix")
+    _call(lib().gdattn_decode_prefix, "gdattn_decode_prefix", device, stream, q.data_ptr(),
+          k_prefix.data_ptr(), _ptr(v_prefix), prefix_len.data_ptr(), rows, k.data_ptr(), _ptr(v),
+          seqlens.data_ptr(), B, T, max_seqlen, ctypes.byref(desc), out.data_ptr(),
+          lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -642,62 +664,60 @@ class RowMap(NamedTuple):
     slot: torch.Tensor   # [n_rows]: its slot in the sequence's cache, or -1
 
 
-def _row_map(batch: int, n_rows: int, device) -> RowMap:
-    flat = torch.empty(batch + 1 + 3 * n_rows, dtype=torch.int32, device=device)
-    return RowMap(*flat.split([batch + 1, n_rows, n_rows, n_rows]))
-
-
 def slot_map(seqlens: torch.Tensor, new_lens: torch.Tensor, n_rows: int, capacity: int,
              n_sink: int = 0, out: Optional[RowMap] = None, stream=None) -> RowMap:
     """gdattn_slot_map: the slots of a step in which new_lens[b] tokens join sequence
     b (seqlens[b] long with them), packed into n_rows rows."""
     B, device = seqlens.numel(), seqlens.device
-    n_rows = int(n_rows)
-    _dense(seqlens, "seqlens", _I32, B, device)
-    _dense(new_lens, "new_lens", _I32, B, device)
+    _need(seqlens, "seqlens", torch.int32, B, device)
+    _need(new_lens, "new_lens", torch.int32, B, device)
+    _on(seqlens, "seqlens", device)
     if n_rows < 0:
         raise ValueError(f"n_rows: {n_rows}")
     if out is None:
-        out = _row_map(B, n_rows, device)
+        flat = torch.empty(B + 1 + 3 * n_rows, dtype=torch.int32, device=device)
+        out = RowMap(*flat.split_with_sizes((B + 1, n_rows, n_rows, n_rows)))
+        start = flat.data_ptr()
+        seq = start + 4 * (B + 1)
+        pos, slot = seq + 4 * n_rows, seq + 8 * n_rows
     else:
-        _dense(out.start, "out.start", _I32, B + 1, device)
+        _need(out.start, "out.start", torch.int32, B + 1, device)
         for name in ("seq", "pos", "slot"):
-            _dense(getattr(out, name), f"out.{name}", _I32, n_rows, device)
-    with _on_device(device):
-        st = lib().gdattn_slot_map(_ptr(seqlens), _ptr(new_lens), B, n_rows, int(capacity),
-                                   int(n_sink), _ptr(out.start), _ptr(out.seq), _ptr(out.pos),
-                                   _ptr(out.slot), _stream_handle(stream))
-    if st != GDATTN_OK:
-        raise GdattnError(st, "gdattn_slot_map")
+            _need(getattr(out, name), f"out.{name}", torch.int32, n_rows, device)
+        start, seq, pos, slot = (t.data_ptr() for t in out)
+    _call(lib().gdattn_slot_map, "gdattn_slot_map", device, stream, seqlens.data_ptr(),
+          new_lens.data_ptr(), B, n_rows, capacity, n_sink, start, seq, pos, slot)
     return out
 
 
 def _row_stride(rows: torch.Tensor, name: str, desc: LayerDesc, n_rows: int, device) -> int:
     """Elements between the rows of a bf16 [n_rows, Hkv, D] tensor whose heads are
     next to one another (a slice of a fused projection is)."""
-    if rows.dtype not in _BF16:
+    H, D = desc.n_kv_heads, desc.head_dim
+    if rows.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: dtype {rows.dtype}, expected torch.bfloat16")
-    H, D = int(desc.n_kv_heads), int(desc.head_dim)
-    if rows.dim() != 3 or tuple(rows.shape[1:]) != (H, D) or rows.shape[0] < n_rows:
+    if rows.dim() != 3 or rows.shape[0] < n_rows or rows.shape[1] != H or rows.shape[2] != D:
         raise ValueError(f"{name}: shape {tuple(rows.shape)}, expected at least {(n_rows, H, D)}")
-    if rows.stride(2) != 1 or (H > 1 and rows.stride(1) != D):
+    stride = rows.stride()
+    if stride[2] != 1 or (H > 1 and stride[1] != D):
         raise ValueError(f"{name}: the heads of a row must be next to one another")
     _on(rows, name, device)
-    return rows.stride(0) if rows.shape[0] > 1 else H * D
+    return stride[0] if rows.shape[0] > 1 else H * D
 
 
 def _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, dtypes):
     """The arguments both cache writes share; returns (n_rows, batch, row stride)."""
     device = k.device
     n_rows, batch = row_slot.numel(), k.shape[0]
-    _dense(row_seq, "row_seq", _I32, n_rows, device)
-    _dense(row_slot, "row_slot", _I32, n_rows, device)
+    _need(row_seq, "row_seq", torch.int32, n_rows, device)
+    _need(row_slot, "row_slot", torch.int32, n_rows, device)
     stride = _row_stride(k_rows, "k_rows", desc, n_rows, device)
-    _extent(k, "k", dtypes, _cache_elems(batch, desc), device)
+    n = _cache_elems(batch, desc)
+    _need_cache(k, "k", dtypes, n, device)
     if v_rows is not None and _row_stride(v_rows, "v_rows", desc, n_rows, device) != stride:
         raise ValueError("v_rows: must have the row stride of k_rows")
     if v is not None:
-        _extent(v, "v", dtypes, _cache_elems(batch, desc), device)
+        _need_cache(v, "v", dtypes, n, device)
     return n_rows, batch, stride
 
 
@@ -714,11 +734,9 @@ def cache_write(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_seq: t
     """gdattn_cache_write: rows bf16 [n_rows, Hkv, D] (any row stride) into the caches
     k, v [B, C, Hkv, D] by a slot map; v_rows and v None when K = V."""
     n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, _BF16)
-    with _on_device(k.device):
-        st = cache_write_raw(_ptr(k_rows), _ptr(v_rows), stride, _ptr(row_seq), _ptr(row_slot),
-                             n_rows, batch, desc, _ptr(k), _ptr(v), _stream_handle(stream))
-    if st != GDATTN_OK:
-        raise GdattnError(st, "gdattn_cache_write")
+    _call(lib().gdattn_cache_write, "gdattn_cache_write", k.device, stream, k_rows.data_ptr(),
+          _ptr(v_rows), stride, row_seq.data_ptr(), row_slot.data_ptr(), n_rows, batch,
+          ctypes.byref(desc), k.data_ptr(), _ptr(v))
 
 
 def cache_write_fp8_raw(k_rows, v_rows, row_stride, row_seq, row_slot, n_rows, batch, desc,
@@ -737,14 +755,12 @@ def cache_write_fp8(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_se
     float8_e4m3fn) and their scales, fp32 [B, Hkv, C]."""
     n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k_codes,
                                          v_codes, _CODES)
-    scales = batch * int(desc.n_kv_heads) * int(desc.cache_capacity)
-    _dense(k_scale, "k_scale", _F32, scales, k_codes.device)
+    device = k_codes.device
+    scales = batch * desc.n_kv_heads * desc.cache_capacity
+    _need(k_scale, "k_scale", torch.float32, scales, device)
     if v_scale is not None:
-        _dense(v_scale, "v_scale", _F32, scales, k_codes.device)
-    with _on_device(k_codes.device):
-        st = cache_write_fp8_raw(_ptr(k_rows), _ptr(v_rows), stride, _ptr(row_seq),
-                                 _ptr(row_slot), n_rows, batch, desc, _ptr(k_codes),
-                                 _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
-                                 _stream_handle(stream))
-    if st != GDATTN_OK:
-        raise GdattnError(st, "gdattn_cache_write_fp8")
+        _need(v_scale, "v_scale", torch.float32, scales, device)
+    _call(lib().gdattn_cache_write_fp8, "gdattn_cache_write_fp8", device, stream,
+          k_rows.data_ptr(), _ptr(v_rows), stride, row_seq.data_ptr(), row_slot.data_ptr(),
+          n_rows, batch, ctypes.byref(desc), k_codes.data_ptr(), _ptr(v_codes),
+          k_scale.data_ptr(), _ptr(v_scale))

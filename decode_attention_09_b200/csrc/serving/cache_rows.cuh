@@ -8,6 +8,15 @@
 
 namespace gdattn {
 
+// 16 bytes that this kernel reads once, past the L1.
+__device__ __forceinline__ uint4 ld_nc_v4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // ------------------------------------------------------------- slot maps
 struct SlotMapParams {
   const int32_t *seqlens;   // [batch], with the step's tokens
@@ -106,80 +115,143 @@ __global__ void __launch_bounds__(kSlotMapThreads) slot_map_kernel(const SlotMap
 
 // ------------------------------------------------------------ cache writes
 struct CacheWriteParams {
-  const uint16_t *rows[2];   // K, V rows (V null: K = V)
-  uint8_t *cache[2];
-  float *scale[2];           // fp8
+  const uint16_t *k_rows, *v_rows;  // v_rows null: K = V
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;         // fp8
   const int32_t *row_seq, *row_slot;
-  int64_t row_stride;        // elements between rows
-  int64_t batch_stride;      // elements between sequences of a cache
+  int64_t row_stride;               // elements between rows
+  int64_t batch_stride;             // elements between sequences of a cache
   int32_t n_rows, batch, capacity, n_kv_heads, head_dim;
 };
 
 constexpr int kCacheWriteThreads = 256;
+constexpr int kCacheWritePieces = 4;  // 16-byte pieces per thread and tensor
 
-// One 16-byte piece of one row per thread and step.
+// Where a row goes: the offset of its cache row in rows, or false.
+__device__ __forceinline__ bool row_target(const CacheWriteParams &p, int32_t r, int32_t &b,
+                                           int32_t &slot) {
+  b = __ldg(p.row_seq + r);
+  slot = __ldg(p.row_slot + r);
+  return b >= 0 && b < p.batch && slot >= 0 && slot < p.capacity;
+}
+
+// A copy, bound by HBM: each thread moves kCacheWritePieces 16-byte pieces of K and
+// as many of V, all loads in flight before the first store.  Rows are read once and
+// never again here, so they pass the L1.
 __global__ void __launch_bounds__(kCacheWriteThreads) cache_write_kernel(const CacheWriteParams p) {
-  const int32_t pieces = p.n_kv_heads * p.head_dim / 8;  // of a row
-  const int64_t total = static_cast<int64_t>(p.n_rows) * pieces;
-  const int w = blockIdx.y;
-  const int64_t row_elems = static_cast<int64_t>(p.n_kv_heads) * p.head_dim;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCacheWriteThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kCacheWriteThreads) {
-    const int32_t r = static_cast<int32_t>(i / pieces), e = static_cast<int32_t>(i % pieces) * 8;
-    const int32_t b = __ldg(p.row_seq + r), slot = __ldg(p.row_slot + r);
-    if (b < 0 || b >= p.batch || slot < 0 || slot >= p.capacity) continue;
-    const uint4 v = *reinterpret_cast<const uint4 *>(p.rows[w] + r * p.row_stride + e);
-    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.cache[w]) + b * p.batch_stride +
-                               slot * row_elems + e) = v;
+  const uint32_t pieces = static_cast<uint32_t>(p.n_kv_heads) * p.head_dim / 8;  // of a row
+  const int64_t row_elems = static_cast<int64_t>(pieces) * 8;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kCacheWriteThreads * kCacheWritePieces);
+  const int32_t r0 = static_cast<int32_t>(first / pieces);
+  const uint32_t e0 = static_cast<uint32_t>(first - static_cast<int64_t>(r0) * pieces);
+  uint4 kx[kCacheWritePieces], vx[kCacheWritePieces];
+  int64_t dst[kCacheWritePieces];
+#pragma unroll
+  for (int j = 0; j < kCacheWritePieces; ++j) {
+    const uint32_t i = e0 + j * kCacheWriteThreads + threadIdx.x;
+    const uint32_t row = i / pieces, e = (i - row * pieces) * 8;
+    const int64_t r = static_cast<int64_t>(r0) + row;
+    dst[j] = -1;
+    int32_t b, slot;
+    if (r < p.n_rows && row_target(p, static_cast<int32_t>(r), b, slot)) {
+      dst[j] = b * p.batch_stride + slot * row_elems + e;
+      kx[j] = ld_nc_v4(p.k_rows + r * p.row_stride + e);
+      if (p.v_rows != nullptr) vx[j] = ld_nc_v4(p.v_rows + r * p.row_stride + e);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kCacheWritePieces; ++j) {
+    if (dst[j] < 0) continue;
+    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.k_cache) + dst[j]) = kx[j];
+    if (p.v_rows != nullptr)
+      *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.v_cache) + dst[j]) = vx[j];
   }
 }
 
-// One warp per (row, KV head): the row's largest magnitude, then its codes.
+// x / s rounded to fp32, r being 1 / s rounded: Markstein's correction (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+// The remainder of the first guess is exact in a fused multiply-add, and the sum is
+// within 2^-47 of the quotient before its one rounding.  That rounding could only go
+// the other way next to a midpoint of fp32, which a bf16 x over a scale that is itself
+// x' / 448 never comes that close to; the tests go through every pair of mantissas.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+
+// Scales that leave the reciprocal, the guess and its remainder (2^-46 of the product)
+// normal, for every quotient that is not far below e4m3's smallest number.
+__device__ __forceinline__ bool plain_scale(float s) { return s > 1e-18f && s < 1e30f; }
+
+// Word w of four (w a constant), two bf16.
+__device__ __forceinline__ uint32_t word(const uint4 &v, int w) {
+  return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+}
+
+// One warp per (row, KV head) at a time, kFp8Rows of them in flight: the row's largest
+// magnitude, then its codes.  Bound by HBM (2 D bytes read, D + 4 written).
+constexpr int kFp8Rows = 4;
 template <int D>
 __global__ void __launch_bounds__(kCacheWriteThreads)
     cache_write_fp8_kernel(const CacheWriteParams p) {
   constexpr int E = D / 32;  // elements per lane: 8 or 16
   const int lane = threadIdx.x & 31;
-  const int w = blockIdx.y;
-  const int64_t total = static_cast<int64_t>(p.n_rows) * p.n_kv_heads;
-  const int64_t row_elems = static_cast<int64_t>(p.n_kv_heads) * D;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kCacheWriteThreads + threadIdx.x) >> 5;
-       i < total; i += static_cast<int64_t>(gridDim.x) * kCacheWriteThreads / 32) {
-    const int32_t r = static_cast<int32_t>(i / p.n_kv_heads);
-    const int32_t h = static_cast<int32_t>(i % p.n_kv_heads);
-    const int32_t b = __ldg(p.row_seq + r), slot = __ldg(p.row_slot + r);
-    if (b < 0 || b >= p.batch || slot < 0 || slot >= p.capacity) continue;
-    const uint16_t *src = p.rows[w] + r * p.row_stride + h * D + lane * E;
-    uint32_t raw[E / 2];
+  const uint16_t *rows = blockIdx.y == 0 ? p.k_rows : p.v_rows;
+  uint8_t *cache = blockIdx.y == 0 ? p.k_cache : p.v_cache;
+  float *scales = blockIdx.y == 0 ? p.k_scale : p.v_scale;
+  const uint32_t H = static_cast<uint32_t>(p.n_kv_heads);
+  const int64_t row_elems = static_cast<int64_t>(H) * D;
+  const int64_t first =
+      (static_cast<int64_t>(blockIdx.x) * (kCacheWriteThreads / 32) + (threadIdx.x >> 5)) * kFp8Rows;
+  const int64_t r0 = first / H;
+  const uint32_t h0 = static_cast<uint32_t>(first - r0 * H);
+  uint4 raw[kFp8Rows][E / 8];
+  int64_t dst[kFp8Rows], sat[kFp8Rows];
 #pragma unroll
-    for (int c = 0; c < E / 8; ++c)
-      *reinterpret_cast<uint4 *>(raw + 4 * c) = *reinterpret_cast<const uint4 *>(src + 8 * c);
-    float x[E], amax = 0.f;
+  for (int j = 0; j < kFp8Rows; ++j) {
+    const uint32_t row = (h0 + j) / H, h = h0 + j - row * H;
+    const int64_t r = r0 + row;
+    dst[j] = -1;
+    int32_t b, slot;
+    if (r < p.n_rows && row_target(p, static_cast<int32_t>(r), b, slot)) {
+      dst[j] = b * p.batch_stride + slot * row_elems + h * D + lane * E;
+      sat[j] = (static_cast<int64_t>(b) * H + h) * p.capacity + slot;
+      const uint16_t *src = rows + r * p.row_stride + h * D + lane * E;
+#pragma unroll
+      for (int c = 0; c < E / 8; ++c) raw[j][c] = ld_nc_v4(src + 8 * c);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kFp8Rows; ++j) {
+    if (dst[j] < 0) continue;  // the whole warp
+    float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < E / 2; ++c) {
-      x[2 * c] = bf16lo(raw[c]);
-      x[2 * c + 1] = bf16hi(raw[c]);
-      amax = fmaxf(amax, fmaxf(fabsf(x[2 * c]), fabsf(x[2 * c + 1])));
+      const uint32_t x = word(raw[j][c / 4], c % 4);
+      amax = fmaxf(amax, fmaxf(fabsf(bf16lo(x)), fabsf(bf16hi(x))));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float scale = __fdiv_rn(amax, 448.f);
-    uint16_t code[E / 2];
+    const bool plain = plain_scale(scale);  // of the whole warp
+    const float inv = plain ? __frcp_rn(scale) : 0.f;
+    uint32_t code[E / 4] = {};
 #pragma unroll
-    for (int c = 0; c < E / 2; ++c)
-      code[c] = scale > 0.f
-                    ? e4m3x2_rn(__fdiv_rn(x[2 * c], scale), __fdiv_rn(x[2 * c + 1], scale))
-                    : static_cast<uint16_t>(0);
-    uint8_t *dst = p.cache[w] + b * p.batch_stride + slot * row_elems + h * D + lane * E;
-#pragma unroll
-    for (int c = 0; c < E / 8; ++c) {
-      uint2 pk;
-      pk.x = code[4 * c] | static_cast<uint32_t>(code[4 * c + 1]) << 16;
-      pk.y = code[4 * c + 2] | static_cast<uint32_t>(code[4 * c + 3]) << 16;
-      *reinterpret_cast<uint2 *>(dst + 8 * c) = pk;
+    for (int c = 0; c < E / 2; ++c) {
+      const uint32_t x = word(raw[j][c / 4], c % 4);
+      uint16_t two = 0;
+      if (plain)
+        two = e4m3x2_rn(quotient(bf16lo(x), scale, inv), quotient(bf16hi(x), scale, inv));
+      else if (scale > 0.f)
+        two = e4m3x2_rn(__fdiv_rn(bf16lo(x), scale), __fdiv_rn(bf16hi(x), scale));
+      code[c / 2] |= static_cast<uint32_t>(two) << (16 * (c % 2));
     }
-    if (lane == 0)
-      p.scale[w][(static_cast<int64_t>(b) * p.n_kv_heads + h) * p.capacity + slot] = scale;
+    if (E == 8)
+      *reinterpret_cast<uint2 *>(cache + dst[j]) = make_uint2(code[0], code[1]);
+    else
+      *reinterpret_cast<uint4 *>(cache + dst[j]) =
+          make_uint4(code[0], code[1], code[E / 4 - 2], code[E / 4 - 1]);
+    if (lane == 0) scales[sat[j]] = scale;
   }
 }
 

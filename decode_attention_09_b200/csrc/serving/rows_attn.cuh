@@ -96,6 +96,7 @@ struct RowsParams {
   float qscale;        // scale * log2(e), or scale / cap with a soft-cap
   float post;          // cap * log2(e), or 0
   int32_t test_withhold;
+  int32_t merge_shares;  // warps that share a row of the merge
 };
 
 // The tensor maps of a call: caches and prefix in boxes of 64 rows and of 16,
@@ -441,25 +442,6 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         if (!mine) continue;
         const RowTile tile = unit_tile(seg.u, t);
         const uint32_t s_col = tmem + lane_base + Cfg::S_COL + sb * TILE;
-        if (ok && tile.ntok < TILE) {
-          // Rows behind the tile's end hold other slots, or what the ring held
-          // before (possibly NaN, which a weight of 0 would not silence): clear
-          // them.  With K = V the tile's Q.K is done: its scores are there.
-          const int st = v_entry<NH, SHARED>(i, tiles) % NST;
-          ok = mbar_wait(SHARED ? &kfull[i & 7] : &vfull[i & 7], (i >> 3) & 1, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            uint8_t *vt = kv + st * Cfg::TB;
-            const int per_box = (TILE - tile.ntok) * 8;
-#pragma unroll 1
-            for (int q = t128; q < per_box; q += 128)
-#pragma unroll
-              for (int box = 0; box < DH / 64; ++box)
-                *reinterpret_cast<uint4 *>(vt + box * Cfg::BOXB + (tile.ntok + (q >> 3)) * 128 +
-                                           (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();  // for the tensor core
-          }
-        }
         if (act) {
           // The tile is walked by 16 columns in loops that stay rolled: the unrolled
           // softmax of 64 columns does not fit the instruction cache beside the other
@@ -609,6 +591,26 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           if (ok) tmem_store_wait();
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         }
+        if (ok && tile.ntok < TILE) {
+          // Rows behind the tile's end hold other slots, or what the ring held
+          // before (possibly NaN, which a weight of 0 would not silence): clear
+          // them.  With K = V the tile's Q.K is done: its scores are there.  Last, so that
+          // a V tile still on its way holds nothing up.
+          const int st = v_entry<NH, SHARED>(i, tiles) % NST;
+          ok = mbar_wait(SHARED ? &kfull[i & 7] : &vfull[i & 7], (i >> 3) & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            uint8_t *vt = kv + st * Cfg::TB;
+            const int per_box = (TILE - tile.ntok) * 8;
+#pragma unroll 1
+            for (int q = t128; q < per_box; q += 128)
+#pragma unroll
+              for (int box = 0; box < DH / 64; ++box)
+                *reinterpret_cast<uint4 *>(vt + box * Cfg::BOXB + (tile.ntok + (q >> 3)) * 128 +
+                                           (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();  // for the tensor core
+          }
+        }
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&pfull[sb]);
@@ -645,36 +647,49 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
                 (seg.prefix ? p.rp : p.rs) + r;
         // Each group writes half of the dims.
         const int d0 = wg * (DH / 2);
-        uint16_t *dst = p.out + orow * Cfg::D + rank * DH + d0;
-        float *part = (seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D + rank * DH + d0;
-        if (ok) tc_fence_after();
-#pragma unroll 1
-        for (int cb = 0; cb < DH / 32; ++cb) {
-          float o[16];
-          if (ok) {
-            tmem_ld16(tmem + lane_base + Cfg::O_COL + d0 + cb * 16, o);
-          } else {
+        uint8_t *base =
+            final_rows
+                ? reinterpret_cast<uint8_t *>(p.out + orow * Cfg::D + rank * DH + d0)
+                : reinterpret_cast<uint8_t *>((seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D +
+                                              rank * DH + d0);
+        // Four lanes swap 32-byte pieces so that each store of theirs is a whole line
+        // of one row (stores of 32 bytes in 32 rows took 7000 cycles for 128 rows).
+        uint8_t *row_base[4];
+        uint32_t row_there = 0;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          row_base[k] = reinterpret_cast<uint8_t *>(__shfl_sync(
+              0xffffffffu, reinterpret_cast<uint64_t>(base), (lane & ~3) + k));
+          row_there |= __shfl_sync(0xffffffffu, row_ok ? 1u : 0u, (lane & ~3) + k) << k;
+        }
+        if (ok) tc_fence_after();
+        const int units = final_rows ? 2 : 4;  // 128-byte lines of a row
+#pragma unroll 1
+        for (int u = 0; u < units; ++u) {
+          uint32_t v[32];
+          if (!ok) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = 0;
+          } else if (final_rows) {
+            float o[64];
+            tmem_ld64(tmem + lane_base + Cfg::O_COL + d0 + u * 64, o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = pack_bf16x2(o[2 * q] * inv, o[2 * q + 1] * inv);
+          } else {
+            float o[32];
+            tmem_load32(tmem + lane_base + Cfg::O_COL + d0 + u * 32, o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(o[q] * inv);
           }
-          if (cb + 1 == DH / 32) {
+          if (u + 1 == units) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(oempty);
           }
-          uint32_t pk[8];
-          if (final_rows) {
+          swap_pieces(v, lane);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
-            if (row_ok) st_global_v8(dst + cb * 16, pk);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 16; q += 8) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) pk[k] = __float_as_uint(o[q + k] * inv);
-              if (row_ok) st_global_v8(part + cb * 16 + q, pk);
-            }
-          }
+          for (int k = 0; k < 4; ++k)
+            if ((row_there >> k) & 1) st_global_v8(row_base[k] + u * 128 + (lane & 3) * 32, v + 8 * k);
         }
         if (row_ok && rank == 0 && have_last) {
           const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;

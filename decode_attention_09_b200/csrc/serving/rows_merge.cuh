@@ -1,9 +1,10 @@
 // Joins the partials that rows_attn.cuh leaves:
 //   lse = log sum_i exp(lse_i),  out = sum_i exp(lse_i - lse) o_i.
-// One warp per output row, a lane owning D / 32 of its dims; the parts' log-sum-exps
-// are read first (one per lane and step), then the parts' rows, eight in flight.
-// Where the parts are is worked out from the lengths before the wait on the kernel
-// in front.  Bound by latency: a few L2 round trips.
+// One to eight warps share an output row (more where there are few rows, whose parts
+// would otherwise be read one after the other: 64 rows of 65 parts at head_dim 512 took
+// 36 us with one warp a row), a lane owning D / 32 of its dims, eight 16-byte loads in
+// flight.  Where the parts are is worked out from the lengths before the wait on the
+// kernel in front.  Bound by latency: a few L2 round trips.
 #pragma once
 
 #include <cstdint>
@@ -24,68 +25,118 @@ struct RowParts {
   }
 };
 
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+
+// What a warp knows of a row after its share of the parts.
 template <int D>
-__device__ __forceinline__ void merge_row(const RowParts (&src)[2], uint16_t *out, float *lse) {
-  constexpr int V = D / 128;  // float4 per lane
+struct RowSum {
+  float4 acc[D / 128];
+  float m, z;
+};
+
+template <int D>
+__device__ __forceinline__ void add_part(RowSum<D> &s, float lse, const float4 (&v)[D / 128]) {
+  if (lse == -INFINITY) return;  // an empty part adds nothing, whatever its row holds
+  const float m = fmaxf(s.m, lse);
+  const float a = exp2f(s.m - m), f = exp2f(lse - m);
+  s.m = m;
+  s.z = fmaf(s.z, a, f);
+#pragma unroll
+  for (int c = 0; c < D / 128; ++c) {
+    s.acc[c].x = fmaf(f, v[c].x, s.acc[c].x * a);
+    s.acc[c].y = fmaf(f, v[c].y, s.acc[c].y * a);
+    s.acc[c].z = fmaf(f, v[c].z, s.acc[c].z * a);
+    s.acc[c].w = fmaf(f, v[c].w, s.acc[c].w * a);
+  }
+}
+
+// Parts share, share + shares, ... of a row.
+template <int D>
+__device__ __forceinline__ RowSum<D> sum_parts(const RowParts (&src)[2], int share, int shares) {
+  constexpr int V = D / 128;       // float4 per lane
+  constexpr int kFlight = 8 / V;   // parts in flight
   const int lane = threadIdx.x & 31;
   const int32_t n0 = src[0].at.n, n = n0 + src[1].at.n;
-  float m = -INFINITY;
-  for (int32_t i = lane; i < n; i += 32) {
-    const RowParts &s = i < n0 ? src[0] : src[1];
-    m = fmaxf(m, __ldcg(s.lse + s.row(i < n0 ? i : i - n0)));
-  }
+  RowSum<D> s;
+  s.m = -INFINITY;
+  s.z = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float4 acc[V];
+  for (int c = 0; c < V; ++c) s.acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int32_t i0 = share; i0 < n; i0 += kFlight * shares) {
+    float lse[kFlight];
+    float4 v[kFlight][V];
 #pragma unroll
-  for (int c = 0; c < V; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float z = 0.f;
-  if (m != -INFINITY) {
-    constexpr int kFlight = 8 / V;
-    for (int32_t i0 = 0; i0 < n; i0 += kFlight) {
-      float w[kFlight];
-      float4 v[kFlight][V];
+    for (int q = 0; q < kFlight; ++q) {
+      const int32_t i = i0 + q * shares;
+      lse[q] = -INFINITY;
+      if (i < n) {
+        const RowParts &from = i < n0 ? src[0] : src[1];
+        const int64_t row = from.row(i < n0 ? i : i - n0);
+        lse[q] = __ldcg(from.lse + row);
 #pragma unroll
-      for (int q = 0; q < kFlight; ++q) {
-        const int32_t i = i0 + q;
-        if (i < n) {
-          const RowParts &s = i < n0 ? src[0] : src[1];
-          const int64_t row = s.row(i < n0 ? i : i - n0);
-          w[q] = __ldcg(s.lse + row);
-#pragma unroll
-          for (int c = 0; c < V; ++c)
-            v[q][c] = __ldcg(reinterpret_cast<const float4 *>(s.o + row * D) + c * 32 + lane);
-        } else {
-          w[q] = -INFINITY;
-        }
+        for (int c = 0; c < V; ++c)
+          v[q][c] = __ldcg(reinterpret_cast<const float4 *>(from.o + row * D) + c * 32 + lane);
       }
+    }
 #pragma unroll
-      for (int q = 0; q < kFlight; ++q) {
-        if (w[q] == -INFINITY) continue;  // an empty part adds nothing
-        const float f = exp2f(w[q] - m);
-        z += f;
+    for (int q = 0; q < kFlight; ++q) add_part<D>(s, lse[q], v[q]);
+  }
+  return s;
+}
+
+// The row's output, by the warps of a CTA that share it (1, 2, 4 or 8 of them, next to
+// one another; every warp of the CTA calls this).
+template <int D>
+__device__ __forceinline__ void merge_row(const RowParts (&src)[2], bool real, int shares,
+                                          uint16_t *out, float *lse) {
+  constexpr int V = D / 128;
+  __shared__ float4 sh_acc[kMergeWarps][D / 4];
+  __shared__ float sh_m[kMergeWarps], sh_z[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = warp % shares;
+  RowSum<D> s = {};
+  if (real) s = sum_parts<D>(src, share, shares);
+  if (shares > 1) {  // of the whole CTA
+    if (share > 0) {
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-          acc[c].x = fmaf(f, v[q][c].x, acc[c].x);
-          acc[c].y = fmaf(f, v[q][c].y, acc[c].y);
-          acc[c].z = fmaf(f, v[q][c].z, acc[c].z);
-          acc[c].w = fmaf(f, v[q][c].w, acc[c].w);
-        }
+      for (int c = 0; c < V; ++c) sh_acc[warp][c * 32 + lane] = s.acc[c];
+      if (lane == 0) {
+        sh_m[warp] = s.m;
+        sh_z[warp] = s.z;
+      }
+    }
+    __syncthreads();
+    if (share > 0) return;
+    for (int w = warp + 1; w < warp + shares; ++w) {
+      // (a share of one part or more: its rows, weighted by its sum)
+      const float mw = sh_m[w], zw = sh_z[w];
+      if (!real || zw == 0.f) continue;
+      const float m = fmaxf(s.m, mw);
+      const float a = exp2f(s.m - m), f = exp2f(mw - m);
+      s.m = m;
+      s.z = s.z * a + zw * f;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float4 v = sh_acc[w][c * 32 + lane];
+        s.acc[c].x = fmaf(f, v.x, s.acc[c].x * a);
+        s.acc[c].y = fmaf(f, v.y, s.acc[c].y * a);
+        s.acc[c].z = fmaf(f, v.z, s.acc[c].z * a);
+        s.acc[c].w = fmaf(f, v.w, s.acc[c].w * a);
       }
     }
   }
-  const float inv = z > 0.f ? __fdividef(1.f, z) : 0.f;
+  if (!real) return;
+  const float inv = s.z > 0.f ? __fdividef(1.f, s.z) : 0.f;
 #pragma unroll
   for (int c = 0; c < V; ++c) {
     uint2 pk;
-    pk.x = pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
-    pk.y = pack_bf16x2(acc[c].z * inv, acc[c].w * inv);
+    pk.x = pack_bf16x2(s.acc[c].x * inv, s.acc[c].y * inv);
+    pk.y = pack_bf16x2(s.acc[c].z * inv, s.acc[c].w * inv);
     *reinterpret_cast<uint2 *>(out + (c * 32 + lane) * 4) = pk;
   }
-  if (lane == 0 && lse != nullptr) *lse = z > 0.f ? (m + log2f(z)) * kLn2 : -INFINITY;
+  if (lane == 0 && lse != nullptr) *lse = s.z > 0.f ? (s.m + log2f(s.z)) * kLn2 : -INFINITY;
 }
-
-constexpr int kMergeThreads = 256;
 
 // Sinks: units that a chunk boundary cuts.  CTA x looks at the boundary behind
 // chunk x and joins the unit there if this is the unit's first boundary.
@@ -104,8 +155,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_cut_units_kernel(const Ro
   grid_dependency_wait();
   if (!cut) return;
   const int32_t nrow = imin32(g.qt_seq, g.tokens - seg.qb * g.qt_seq) * g.group;
-  const int32_t r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (r >= nrow) return;
+  const int32_t r = blockIdx.y * (kMergeWarps / p.merge_shares) + (threadIdx.x >> 5) / p.merge_shares;
   src[0].o = p.own_o;
   src[0].lse = p.own_lse;
   src[0].rows = p.rs;
@@ -113,7 +163,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_cut_units_kernel(const Ro
   const int32_t tq = r / g.group, h = r - tq * g.group;
   const int64_t row = (static_cast<int64_t>(seg.qb * g.qt_seq + tq) * g.batch + seg.b) *
                           (g.n_kv_heads * g.group) + seg.x * g.group + h;
-  merge_row<D>(src, p.out + row * D, p.lse != nullptr ? p.lse + row : nullptr);
+  merge_row<D>(src, r < nrow, p.merge_shares, p.out + row * D,
+               p.lse != nullptr ? p.lse + row : nullptr);
 }
 
 // Prefix: every output row has parts of its prefix unit and of its own unit.
@@ -122,7 +173,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_prefix_kernel(const RowsP
   const RowsGeom &g = p.g;
   const int lane = threadIdx.x & 31;
   const int32_t Hq = g.n_kv_heads * g.group;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeWarps / p.merge_shares) +
+                      (threadIdx.x >> 5) / p.merge_shares;
   const bool real = row < static_cast<int64_t>(g.tokens) * g.batch * Hq;
   const int64_t safe = real ? row : 0;
   const int32_t a = static_cast<int32_t>(safe / Hq), hq = static_cast<int32_t>(safe % Hq);
@@ -154,7 +206,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_prefix_kernel(const RowsP
   src[1].r = (tok - qb * g.qt_seq) * g.group + h;
   grid_launch_dependents();
   grid_dependency_wait();
-  if (real) merge_row<D>(src, p.out + row * D, p.lse != nullptr ? p.lse + row : nullptr);
+  merge_row<D>(src, real, p.merge_shares, p.out + row * D,
+               p.lse != nullptr ? p.lse + row : nullptr);
 }
 
 }  // namespace gdattn

@@ -36,15 +36,56 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const float (&v)[16
       : "memory");
 }
 
+// 32 consecutive columns of this thread's TMEM lane; load and wait in one statement.
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ void tmem_store_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // 32 bytes to global memory (32-byte aligned): one sector per lane.
-__device__ __forceinline__ void st_global_v8(void *dst, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void st_global_v8(void *dst, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+// Four neighbouring lanes with four pieces of 8 words each: afterwards lane j holds,
+// as piece k, piece j of lane k.
+__device__ __forceinline__ void swap_pieces(uint32_t (&v)[32], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & bit) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t &lo = v[8 * a + i], &hi = v[8 * (a | bit) + i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+        if (up)
+          lo = got;
+        else
+          hi = got;
+      }
+    }
+  }
 }
 
 // The two warps that share rows (64 threads), on named barrier `id`.

@@ -22,6 +22,8 @@ namespace {
 constexpr int32_t kMaxRowsTokens = 1 << 20;
 constexpr int32_t kMaxGroup = 128;  // query heads per KV head: one block of query rows
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // What both attention entry points check of the pointers (the workspace aside).
@@ -164,18 +166,18 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
 template <int D>
 cudaError_t launch_merge(const RowsLayout &lay, const RowsParams &p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
-  constexpr int kRows = kMergeThreads / 32;
+  const int rows_per_cta = kMergeWarps / p.merge_shares;  // of a CTA
   if (lay.g.prefix_len != nullptr) {
     const int64_t rows =
         static_cast<int64_t>(lay.g.batch) * lay.g.tokens * lay.g.n_kv_heads * lay.g.group;
-    cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),
+    cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>((rows + rows_per_cta - 1) / rows_per_cta)),
                                            kMergeThreads, 0, stream, attr);
     return cudaLaunchKernelEx(&cfg, merge_prefix_kernel<D>, p);
   }
   if (lay.workers == 1) return cudaSuccess;  // no boundary
   cudaLaunchConfig_t cfg =
       launch_config(dim3(static_cast<unsigned>(lay.workers - 1),
-                         static_cast<unsigned>((lay.rs + kRows - 1) / kRows)),
+                         static_cast<unsigned>((lay.rs + rows_per_cta - 1) / rows_per_cta)),
                     kMergeThreads, 0, stream, attr);
   return cudaLaunchKernelEx(&cfg, merge_cut_units_kernel<D>, p);
 }
@@ -233,6 +235,13 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   p.qscale = desc->softcap > 0.f ? desc->scale / desc->softcap : desc->scale * log2e;
   p.post = desc->softcap > 0.f ? desc->softcap * log2e : 0.f;
   p.test_withhold = (desc->flags & GDATTN_FLAG_TEST_WITHHOLD_KV) ? 1 : 0;
+  // Warps per row of the merge: enough to fill the SMs twice over, where the rows do not.
+  const int64_t merge_rows = prefix_len != nullptr
+                                 ? static_cast<int64_t>(g.batch) * g.tokens * Hq
+                                 : static_cast<int64_t>(lay.workers) * lay.rs;
+  p.merge_shares = 1;
+  while (p.merge_shares < kMergeWarps && merge_rows * p.merge_shares < 148 * 2 * kMergeWarps)
+    p.merge_shares *= 2;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = rows_launch(lay.nh, lay.workers, stream, attr);
   if (cudaLaunchKernelEx(&cfg, rows_kernel(desc), m, p) != cudaSuccess) return GDATTN_ERR_CUDA;
@@ -270,10 +279,10 @@ CacheWriteParams write_params(const void *k_rows, const void *v_rows, int64_t ro
                               int32_t batch, const gdattn_layer_desc *desc, void *k_cache,
                               void *v_cache) {
   CacheWriteParams p = {};
-  p.rows[0] = static_cast<const uint16_t *>(k_rows);
-  p.rows[1] = static_cast<const uint16_t *>(v_rows);
-  p.cache[0] = static_cast<uint8_t *>(k_cache);
-  p.cache[1] = static_cast<uint8_t *>(v_cache);
+  p.k_rows = static_cast<const uint16_t *>(k_rows);
+  p.v_rows = static_cast<const uint16_t *>(v_rows);
+  p.k_cache = static_cast<uint8_t *>(k_cache);
+  p.v_cache = static_cast<uint8_t *>(v_cache);
   p.row_seq = row_seq;
   p.row_slot = row_slot;
   p.row_stride = row_stride;
@@ -286,11 +295,6 @@ CacheWriteParams write_params(const void *k_rows, const void *v_rows, int64_t ro
   p.n_kv_heads = desc->n_kv_heads;
   p.head_dim = desc->head_dim;
   return p;
-}
-
-unsigned write_grid(int64_t items, int64_t per_cta) {
-  const int64_t n = (items + per_cta - 1) / per_cta;
-  return static_cast<unsigned>(n < 1 ? 1 : (n < 148 * 16 ? n : 148 * 16));
 }
 
 }  // namespace
@@ -392,10 +396,10 @@ gdattn_status gdattn_cache_write(const void *k_rows, const void *v_rows, int64_t
   if (n_rows == 0) return GDATTN_OK;
   const CacheWriteParams p = write_params(k_rows, v_rows, row_stride, row_seq, row_slot, n_rows,
                                           batch, desc, k_cache, v_cache);
-  const dim3 grid(write_grid(static_cast<int64_t>(n_rows) * desc->n_kv_heads * desc->head_dim / 8,
-                             kCacheWriteThreads),
-                  v_rows ? 2 : 1);
-  cache_write_kernel<<<grid, kCacheWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const int64_t pieces = static_cast<int64_t>(n_rows) * desc->n_kv_heads * desc->head_dim / 8;
+  const int64_t grid = ceil_div(pieces, kCacheWriteThreads * kCacheWritePieces);
+  if (grid > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
+  cache_write_kernel<<<static_cast<unsigned>(grid), kCacheWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? GDATTN_OK : GDATTN_ERR_CUDA;
 }
 
@@ -414,11 +418,12 @@ gdattn_status gdattn_cache_write_fp8(const void *k_rows, const void *v_rows, int
   if (n_rows == 0) return GDATTN_OK;
   CacheWriteParams p = write_params(k_rows, v_rows, row_stride, row_seq, row_slot, n_rows, batch,
                                     desc, k_codes, v_codes);
-  p.scale[0] = k_scale;
-  p.scale[1] = v_scale;
-  const dim3 grid(write_grid(static_cast<int64_t>(n_rows) * desc->n_kv_heads,
-                             kCacheWriteThreads / 32),
-                  v_rows ? 2 : 1);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  const int64_t ctas = ceil_div(static_cast<int64_t>(n_rows) * desc->n_kv_heads,
+                                kCacheWriteThreads / 32 * kFp8Rows);
+  if (ctas > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(ctas), v_rows ? 2 : 1);
   if (desc->head_dim == 256)
     cache_write_fp8_kernel<256>
         <<<grid, kCacheWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);

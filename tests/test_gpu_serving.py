@@ -257,3 +257,30 @@ def test_rows_out_of_range_are_skipped():
     want = torch.ones((B, C, H, D), dtype=torch.bfloat16)
     want[0, 0] = rows[0].cpu()
     assert torch.equal(cache.t.cpu(), want)
+
+
+def test_fp8_codes_of_every_pair_of_mantissas():
+    """The kernel's division against the definition for every mantissa of a row's
+    largest magnitude, every mantissa of a value and the exponents down to zero codes,
+    at scales of ordinary size and at the ends of fp32's range."""
+    H, D = 1, 256
+    m = torch.arange(128, dtype=torch.float64)
+    big = 1 + m / 128                       # every bf16 mantissa
+    rows = []
+    for shift in (0, -100, 120):            # exponent of the row
+        for e in range(0, 20):              # the values' exponents below it
+            x = torch.cat([big[:, None], -(big[None, :] * 2.0 ** -e).expand(128, -1)], 1)
+            x[:, 1:] = torch.where(x[:, 1:].abs() > big[:, None], -0.5 * big[:, None], x[:, 1:])
+            rows.append(torch.cat([x, x[:, 1:].abs(), x[:, :0]], 1)[:, :256] * 2.0 ** shift)
+    rows = torch.cat(rows).to(torch.bfloat16)
+    rows = torch.cat([rows, torch.zeros(rows.shape[0], D - rows.shape[1], dtype=torch.bfloat16)], 1)
+    n = rows.shape[0]
+    desc = binding.make_desc(1, H, D, 0, 0.0, 1.0, True, n)
+    codes = torch.zeros((1, n, H, D), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((1, H, n), device="cuda")
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    binding.cache_write_fp8(rows.cuda().view(n, H, D), None, torch.zeros_like(at), at, desc, codes,
+                            None, scale)
+    value, s = ref.e4m3_rows(rows)
+    assert torch.equal(scale.cpu().view(-1).double(), s)
+    assert torch.equal(codes.cpu().view(n, D).view(torch.float8_e4m3fn).double(), value)
