@@ -42,8 +42,8 @@
 // next.  kfull, vfull: their eight uses back tile i - 8's products are done.  odone of tile j: Q.K of tile j waited for the use before it, and whoever
 // waits has seen tile j's scores; it cannot complete again before tile j + 4, which
 // needs the waiter's own weights.  refset: the two groups alternate inside a
-// segment and meet at its end.  oempty: every warp arrives behind the segment's
-// last P.V, whose first one waited for the phase before.
+// segment and meet at its end.  oempty: a group arrives behind the segment's last
+// P.V, whose first one waited for the phase before.
 #pragma once
 
 #include <cstdint>
@@ -108,18 +108,18 @@ struct RowsMaps {
 };
 
 // Ring entry of tile i's K: with separate tensors K_0 .. K_a are followed by V_0,
-// K_(a+1), V_1 and so on (a = kAhead, fewer where the chunk has fewer tiles); with
-// K = V there is one entry a tile.
+// K_(a+1), V_1 and so on (a = kAhead); with K = V there is one entry a tile.
 template <int NH, bool SHARED>
 __device__ __forceinline__ uint32_t k_entry(uint32_t i) {
   constexpr uint32_t a = RowsConfig<NH>::kAhead;
   return SHARED ? i : (i <= a ? i : 2 * i - a);
 }
-// And of its V, in a chunk of n tiles: one behind K_(i + a), or behind all K.
+// And of its V: one behind K_(i + a).  Behind a chunk's last K the entries of the K
+// that would follow stay unused; no later entry takes their slots.
 template <int NH, bool SHARED>
-__device__ __forceinline__ uint32_t v_entry(uint32_t i, uint32_t n) {
+__device__ __forceinline__ uint32_t v_entry(uint32_t i) {
   constexpr uint32_t a = RowsConfig<NH>::kAhead;
-  return SHARED ? i : (i + a < n ? 2 * i + a + 1 : n + i);
+  return SHARED ? i : 2 * i + a + 1;
 }
 
 template <int NH, bool SHARED, bool CAP>
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       mbar_init(&qempty[s], 1);
       mbar_init(&drain[s], 1);
     }
-    mbar_init(oempty, 8);
+    mbar_init(oempty, 4);
     for (int s = 0; s < 8; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&vfull[s], 1);
@@ -206,7 +206,6 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_base_smem;
   const RowsPlan plan = *plan_smem;
-  const uint32_t tiles = static_cast<uint32_t>(plan.ce - plan.cs);  // of this worker
   RowSegments segs;
   segs.init(g, plan);
   RowSegment seg;
@@ -217,10 +216,10 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     if (plan.bad && worker == 0 && rank == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
     const uint64_t pol = l2_evict_first_policy();
     bool ok = true;
-    uint32_t e = 0;            // ring entries so far
-    uint32_t nk = 0, nv = 0;   // tiles whose K, V were loaded
+    uint32_t nk = 0, nv = 0;  // tiles whose K, V were loaded
     auto load = [&](const RowSegment &sg, int32_t t, bool is_v) {
       const RowTile tile = unit_tile(sg.u, t);
+      const uint32_t e = is_v ? v_entry<NH, SHARED>(nv) : k_entry<NH, SHARED>(nk);
       const int st = e % NST;
       if (e >= NST) ok = mbar_wait(&empty[st], ((e / NST) - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
@@ -246,7 +245,6 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         }
       }
       __syncwarp();
-      ++e;
       ++(is_v ? nv : nk);
     };
     if (SHARED) {
@@ -357,7 +355,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     uint32_t i = 0, n = 0;
     for (; ok && segs.next(g, seg); ++n) {
       for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
-        const int st = v_entry<NH, SHARED>(i, tiles) % NST, pb = i & 3;
+        const int st = v_entry<NH, SHARED>(i) % NST, pb = i & 3;
         // The first product of a block overwrites O: its last block was read.
         if (t == seg.t0 && n > 0) ok = mbar_wait(oempty, (n - 1) & 1, abort_flag, p.status);
         if (ok) ok = mbar_wait(&pfull[pb], (i >> 2) & 1, abort_flag, p.status);
@@ -405,6 +403,13 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     uint32_t i = 0;       // tiles so far
     uint32_t n_own = 0;   // references this warp set
     uint32_t n_other = 0; // references the other group's warp set, up to this tile
+    // Behind a segment whose last tile was the other group's, that group reads the sum
+    // this warp left in ref_own: wait for it before the slot is written again.
+    bool lent = false;
+    auto take_back_ref = [&]() {
+      if (lent) pair_sync(5 + qd);
+      lent = false;
+    };
     while (segs.next(g, seg)) {
       // The row: its token, sequence and head, and the positions it sees.
       const int32_t qt = seg.prefix ? g.qt_pre : g.qt_seq;
@@ -430,16 +435,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;  // l: sum of this group's weights, for m_ref
       for (int32_t t = seg.t0; t < seg.t1; ++t, ++i) {
         const int sb = i & 3;
-        const bool mine = static_cast<int>(i & 1) == wg;
-        if (!mine && act) {
-          ++n_other;
+        if (static_cast<int>(i & 1) != wg) {
+          if (act) ++n_other;
           continue;
         }
-        // (A warp without rows waits for the other group's tiles too: it has nothing
-        // else that keeps it from running segments ahead of the barriers' phases.)
         if (ok) ok = mbar_wait(&sfull[sb], (i >> 2) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (!mine) continue;
         const RowTile tile = unit_tile(seg.u, t);
         const uint32_t s_col = tmem + lane_base + Cfg::S_COL + sb * TILE;
         if (act) {
@@ -548,6 +549,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             }
           }
           const float now = moved ? mx : prev;
+          take_back_ref();
           *ref_own = now;
           __syncwarp();
           if (lane == 0) mbar_arrive(set_own);
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // before (possibly NaN, which a weight of 0 would not silence): clear
           // them.  With K = V the tile's Q.K is done: its scores are there.  Last, so that
           // a V tile still on its way holds nothing up.
-          const int st = v_entry<NH, SHARED>(i, tiles) % NST;
+          const int st = v_entry<NH, SHARED>(i) % NST;
           ok = mbar_wait(SHARED ? &kfull[i & 7] : &vfull[i & 7], (i >> 3) & 1, abort_flag, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
@@ -615,25 +617,27 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&pfull[sb]);
       }
-      // --- the rows' output: final, or a partial of its unit.  The group of the
-      // last tile has the final reference; the sums are joined over ref[].
+      // --- the rows' output, by the group of the segment's last tile, which has the
+      // final reference; the other leaves its sum in ref[] and goes on to the next
+      // segment's first tile.
       const bool have_last = static_cast<int>((i - 1) & 1) == wg;
-      if (act) {
-        if (!have_last) {
+      if (!have_last) {
+        if (act) {
           // (n_other counts the last tile's)
           if (ok) ok = mbar_wait(set_other, (n_other - 1) & 1, abort_flag, p.status);
           ok = __all_sync(0xffffffffu, ok);
           const float last = ok ? *ref_other : m_ref;
+          take_back_ref();
           *ref_own = m_ref == -INFINITY ? 0.f : l * exp2f(m_ref - last);
-          m_ref = last;
+          pair_arrive(1 + qd);
+          lent = true;
         }
+        continue;
+      }
+      if (act) {
         pair_sync(1 + qd);
-        if (have_last) {
-          l += *ref_other;
-          *ref_own = l;
-        }
-        pair_sync(1 + qd);
-        if (!have_last) l = *ref_other;
+        l += *ref_other;
+        pair_arrive(5 + qd);
       }
       if (ok) ok = mbar_wait(&odone[(i - 1) & 3], ((i - 1) >> 2) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
@@ -645,13 +649,11 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         const int64_t prow =
             partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens) *
                 (seg.prefix ? p.rp : p.rs) + r;
-        // Each group writes half of the dims.
-        const int d0 = wg * (DH / 2);
         uint8_t *base =
             final_rows
-                ? reinterpret_cast<uint8_t *>(p.out + orow * Cfg::D + rank * DH + d0)
+                ? reinterpret_cast<uint8_t *>(p.out + orow * Cfg::D + rank * DH)
                 : reinterpret_cast<uint8_t *>((seg.prefix ? p.pre_o : p.own_o) + prow * Cfg::D +
-                                              rank * DH + d0);
+                                              rank * DH);
         // Four lanes swap 32-byte pieces so that each store of theirs is a whole line
         // of one row (stores of 32 bytes in 32 rows took 7000 cycles for 128 rows).
         uint8_t *row_base[4];
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           row_there |= __shfl_sync(0xffffffffu, row_ok ? 1u : 0u, (lane & ~3) + k) << k;
         }
         if (ok) tc_fence_after();
-        const int units = final_rows ? 2 : 4;  // 128-byte lines of a row
+        const int units = final_rows ? DH / 64 : DH / 32;  // 128-byte lines of a row
 #pragma unroll 1
         for (int u = 0; u < units; ++u) {
           uint32_t v[32];
@@ -672,12 +674,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             for (int q = 0; q < 32; ++q) v[q] = 0;
           } else if (final_rows) {
             float o[64];
-            tmem_ld64(tmem + lane_base + Cfg::O_COL + d0 + u * 64, o);
+            tmem_ld64(tmem + lane_base + Cfg::O_COL + u * 64, o);
 #pragma unroll
             for (int q = 0; q < 32; ++q) v[q] = pack_bf16x2(o[2 * q] * inv, o[2 * q + 1] * inv);
           } else {
             float o[32];
-            tmem_load32(tmem + lane_base + Cfg::O_COL + d0 + u * 32, o);
+            tmem_load32(tmem + lane_base + Cfg::O_COL + u * 32, o);
 #pragma unroll
             for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(o[q] * inv);
           }
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           for (int k = 0; k < 4; ++k)
             if ((row_there >> k) & 1) st_global_v8(row_base[k] + u * 128 + (lane & 3) * 32, v + 8 * k);
         }
-        if (row_ok && rank == 0 && have_last) {
+        if (row_ok && rank == 0) {
           const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
           if (!final_rows)
             (seg.prefix ? p.pre_lse : p.own_lse)[prow] = lse2;
@@ -702,6 +704,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         mbar_arrive(oempty);
       }
     }
+    take_back_ref();
   }
 
   tc_fence_before();

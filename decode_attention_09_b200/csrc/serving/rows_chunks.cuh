@@ -1,11 +1,12 @@
-// Split of a call's tiles over the CTAs (or CTA pairs) of the grid.
+// Split of a call's work over the CTAs (or CTA pairs) of the grid.
 //
-// All units' tiles are laid end to end: first the prefix units, unit
+// A unit takes unit_cost steps (starting a block, writing its rows) and then one step
+// per tile.  All units' steps are laid end to end: first the prefix units, unit
 // u = x * npb + pb (KV head x, prefix block pb), then the own units, unit
 // y * Hkv + x for pair y = b * nqb + qb (sequence b, its block qb).  The whole is
 // cut into equal chunks, one per worker (a CTA or a CTA pair), whatever the mix
 // of lengths: the lengths are read on the device, so a captured graph follows
-// them and the host never waits.  The piece of a unit in a chunk is a segment.
+// them and the host never waits.  The tiles of a unit in a chunk are a segment.
 #pragma once
 
 #include <cstdint>
@@ -16,12 +17,12 @@
 namespace gdattn {
 
 struct RowsPlan {
-  int64_t total;      // tiles
-  int64_t chunk;      // tiles per worker
-  int64_t cs, ce;     // this worker's tiles
-  int64_t prefix_all; // tiles of all prefix units
-  int64_t y_start;    // first tile of pair y
-  int32_t y;          // the own pair that tile max(cs, prefix_all) is in
+  int64_t total;      // steps
+  int64_t chunk;      // steps per worker
+  int64_t cs, ce;     // this worker's steps
+  int64_t prefix_all; // steps of all prefix units
+  int64_t y_start;    // first step of pair y
+  int32_t y;          // the own pair that step max(cs, prefix_all) is in
   int32_t prefix_len; // P
   int32_t least_own;
   int32_t bad;
@@ -33,9 +34,15 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
-__device__ __forceinline__ int32_t pair_tiles(const RowsGeom &g, int32_t y, bool &bad) {
+// Steps of a unit of pair y.
+__device__ __forceinline__ int32_t pair_steps(const RowsGeom &g, int32_t y, bool &bad) {
   const int32_t b = y / g.nqb;
-  return own_unit(g, __ldg(g.seqlens + b), y - b * g.nqb, bad).n;
+  return own_unit(g, __ldg(g.seqlens + b), y - b * g.nqb, bad).n + g.unit_cost;
+}
+
+// And of a prefix unit (none when there is nothing to read).
+GDATTN_HD int32_t prefix_steps(const RowsGeom &g, const UnitTiles &pu) {
+  return pu.n > 0 ? pu.n + g.unit_cost : 0;
 }
 
 // The plan of worker c of `workers`; run by one whole warp, every lane gets it.
@@ -45,7 +52,7 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
   RowsPlan p;
   bool bad = false;
   int64_t own = 0;
-  for (int32_t y = lane; y < pairs; y += 32) own += pair_tiles(g, y, bad);
+  for (int32_t y = lane; y < pairs; y += 32) own += pair_steps(g, y, bad);
   own = warp_sum64(own) * g.n_kv_heads;
   p.prefix_len = 0;
   p.least_own = 0;
@@ -63,15 +70,16 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
         least = imin32(least, __shfl_xor_sync(0xffffffffu, least, o));
     }
     p.least_own = least == INT32_MAX ? 0 : least;
-    p.prefix_all = static_cast<int64_t>(prefix_unit(g, p.prefix_len, p.least_own).n) *
-                   g.n_kv_heads * g.npb;
+    p.prefix_all =
+        static_cast<int64_t>(prefix_steps(g, prefix_unit(g, p.prefix_len, p.least_own))) *
+        g.n_kv_heads * g.npb;
   }
   p.bad = __any_sync(0xffffffffu, bad);
   p.total = p.prefix_all + own;
   p.chunk = (p.total + workers - 1) / workers;
   p.cs = p.chunk * c < p.total ? p.chunk * c : p.total;
   p.ce = p.cs + p.chunk < p.total ? p.cs + p.chunk : p.total;
-  // The own pair whose tiles reach past the chunk's start.
+  // The own pair whose steps reach past the chunk's start.
   p.y = 0;
   p.y_start = p.prefix_all;
   if (p.cs > p.prefix_all) {
@@ -81,7 +89,7 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
       const int32_t y = y0 + lane;
       bool dummy = false;
       const int64_t span =
-          y < pairs ? static_cast<int64_t>(pair_tiles(g, y, dummy)) * g.n_kv_heads : 0;
+          y < pairs ? static_cast<int64_t>(pair_steps(g, y, dummy)) * g.n_kv_heads : 0;
       int64_t incl = span;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -102,7 +110,7 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
   return p;
 }
 
-// One (chunk, unit) piece of work: tiles [t0, t1) of the unit.
+// One (chunk, unit) piece of work: tiles [t0, t1) of the unit, at least one.
 struct RowSegment {
   UnitTiles u;
   int32_t t0, t1;
@@ -110,6 +118,7 @@ struct RowSegment {
   int32_t b, qb;   // own: sequence and block; prefix: qb is the prefix block
   int32_t unit;    // index among the prefix units, or among the own units
   int32_t L;       // own: the sequence's length
+  int64_t start;   // the unit's first step
   bool prefix;
   bool opens;      // first segment of its chunk
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.n; }
@@ -131,42 +140,43 @@ struct RowSegments {
   }
 
   __device__ __forceinline__ bool next(const RowsGeom &g, RowSegment &s) {
-    if (pos >= ce) return false;
-    s.opens = pos == cs;
-    if (pos < prefix_all) {
-      s.prefix = true;
-      s.u = pu;
-      s.unit = static_cast<int32_t>(pos / pu.n);
-      s.x = s.unit / g.npb;
-      s.qb = s.unit - s.x * g.npb;
-      s.b = 0;
-      s.L = 0;
-      const int64_t start = static_cast<int64_t>(s.unit) * pu.n;
-      s.t0 = static_cast<int32_t>(pos - start);
-      s.t1 = static_cast<int32_t>(ce - start < pu.n ? ce - start : pu.n);
-      pos = start + s.t1;
-      return true;
-    }
     const int32_t pairs = g.batch * g.nqb;
-    for (; y < pairs; ++y) {
-      bool dummy = false;
-      s.b = y / g.nqb;
-      s.qb = y - s.b * g.nqb;
-      s.L = __ldg(g.seqlens + s.b);
-      s.u = own_unit(g, s.L, s.qb, dummy);
-      const int64_t span = static_cast<int64_t>(s.u.n) * g.n_kv_heads;
-      if (y_start + span > pos) break;
-      y_start += span;
+    while (pos < ce) {
+      if (pos < prefix_all) {
+        const int32_t steps = prefix_steps(g, pu);
+        s.prefix = true;
+        s.u = pu;
+        s.unit = static_cast<int32_t>(pos / steps);
+        s.x = s.unit / g.npb;
+        s.qb = s.unit - s.x * g.npb;
+        s.b = 0;
+        s.L = 0;
+        s.start = static_cast<int64_t>(s.unit) * steps;
+      } else {
+        for (; y < pairs; ++y) {
+          bool dummy = false;
+          s.b = y / g.nqb;
+          s.qb = y - s.b * g.nqb;
+          s.L = __ldg(g.seqlens + s.b);
+          s.u = own_unit(g, s.L, s.qb, dummy);
+          const int64_t span = static_cast<int64_t>(s.u.n + g.unit_cost) * g.n_kv_heads;
+          if (y_start + span > pos) break;
+          y_start += span;
+        }
+        if (y >= pairs) return false;
+        s.prefix = false;
+        s.x = static_cast<int32_t>((pos - y_start) / (s.u.n + g.unit_cost));
+        s.unit = y * g.n_kv_heads + s.x;
+        s.start = y_start + static_cast<int64_t>(s.x) * (s.u.n + g.unit_cost);
+      }
+      const int64_t first = s.start + g.unit_cost;  // its first tile's step
+      s.opens = s.start <= cs;
+      s.t0 = pos > first ? static_cast<int32_t>(pos - first) : 0;
+      s.t1 = ce <= first ? 0 : ce - first < s.u.n ? static_cast<int32_t>(ce - first) : s.u.n;
+      pos = first + s.u.n < ce ? first + s.u.n : ce;
+      if (s.t1 > s.t0) return true;  // (else the chunk ends in front of the first tile)
     }
-    if (y >= pairs) return false;
-    s.prefix = false;
-    s.x = static_cast<int32_t>((pos - y_start) / s.u.n);
-    s.unit = y * g.n_kv_heads + s.x;
-    const int64_t start = y_start + static_cast<int64_t>(s.x) * s.u.n;
-    s.t0 = static_cast<int32_t>(pos - start);
-    s.t1 = static_cast<int32_t>(ce - start < s.u.n ? ce - start : s.u.n);
-    pos = start + s.t1;
-    return true;
+    return false;
   }
 };
 
@@ -186,10 +196,10 @@ struct PartSlots {
   int32_t n;
 };
 
-// Call with a prefix: a unit of its kind that starts at tile `start` and has n > 0.
-GDATTN_HD PartSlots unit_parts(int64_t chunk, int64_t start, int32_t n, int32_t unit) {
-  const int32_t cf = static_cast<int32_t>(start / chunk);
-  const int32_t cl = static_cast<int32_t>((start + n - 1) / chunk);
+// Call with a prefix: a unit of its kind whose n > 0 tiles start at step `first`.
+GDATTN_HD PartSlots unit_parts(int64_t chunk, int64_t first, int32_t n, int32_t unit) {
+  const int32_t cf = static_cast<int32_t>(first / chunk);
+  const int32_t cl = static_cast<int32_t>((first + n - 1) / chunk);
   PartSlots s;
   s.n = cl - cf + 1;
   s.step = 1;
@@ -198,15 +208,15 @@ GDATTN_HD PartSlots unit_parts(int64_t chunk, int64_t start, int32_t n, int32_t 
   return s;
 }
 
-// Call without a prefix: whether the boundary behind chunk c is the first one
-// inside a unit, and that unit's pieces.  seg: the first segment of chunk c + 1
-// (there must be one), which starts at tile `cs`.
-GDATTN_HD bool cut_parts(int64_t chunk, int32_t c, int64_t cs, int32_t t0, int32_t n,
+// Call without a prefix: whether the boundary behind chunk c is the first one among
+// the tiles of the unit that starts at step `start` and has n tiles, and its pieces.
+GDATTN_HD bool cut_parts(int64_t chunk, int32_t c, int64_t start, int32_t unit_cost, int32_t n,
                          PartSlots &s) {
-  if (t0 == 0 || t0 > chunk) return false;  // cut by an earlier boundary, or not at all
-  const int64_t start = cs - t0;
-  s.n = static_cast<int32_t>((start + n - 1) / chunk) - c + 1;
-  s.first = partial_slot(false, c, 0, start == chunk * c);
+  const int64_t first = start + unit_cost, here = chunk * (c + 1);
+  if (first >= here || here >= first + n) return false;  // not among its tiles
+  if (first < chunk * c) return false;                   // cut by an earlier boundary
+  s.n = static_cast<int32_t>((first + n - 1) / chunk) - c + 1;
+  s.first = partial_slot(false, c, 0, start <= chunk * c);
   s.next = partial_slot(false, c + 1, 0, true);
   s.step = 2;
   return true;

@@ -2,8 +2,8 @@
 //   lse = log sum_i exp(lse_i),  out = sum_i exp(lse_i - lse) o_i.
 // One to eight warps share an output row (more where there are few rows, whose parts
 // would otherwise be read one after the other: 64 rows of 65 parts at head_dim 512 took
-// 36 us with one warp a row), a lane owning D / 32 of its dims, eight 16-byte loads in
-// flight.  Where the parts are is worked out from the lengths before the wait on the
+// 36 us with one warp a row), a lane owning D / 32 of its dims, sixteen 16-byte loads
+// in flight.  Where the parts are is worked out from the lengths before the wait on the
 // kernel in front.  Bound by latency: a few L2 round trips.
 #pragma once
 
@@ -55,7 +55,7 @@ __device__ __forceinline__ void add_part(RowSum<D> &s, float lse, const float4 (
 template <int D>
 __device__ __forceinline__ RowSum<D> sum_parts(const RowParts (&src)[2], int share, int shares) {
   constexpr int V = D / 128;       // float4 per lane
-  constexpr int kFlight = 8 / V;   // parts in flight
+  constexpr int kFlight = 16 / V;  // parts in flight
   const int lane = threadIdx.x & 31;
   const int32_t n0 = src[0].at.n, n = n0 + src[1].at.n;
   RowSum<D> s;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_cut_units_kernel(const Ro
   RowSegment seg;
   RowParts src[2] = {};
   const bool cut =
-      segs.next(g, seg) && cut_parts(pl.chunk, c, pl.cs, seg.t0, seg.u.n, src[0].at);
+      segs.next(g, seg) && cut_parts(pl.chunk, c, seg.start, g.unit_cost, seg.u.n, src[0].at);
   grid_launch_dependents();
   grid_dependency_wait();
   if (!cut) return;
@@ -190,18 +190,20 @@ __global__ void __launch_bounds__(kMergeThreads) merge_prefix_kernel(const RowsP
   if (pu.n > 0) {
     const int32_t pb = a / g.qt_pre;
     const int32_t unit = x * g.npb + pb;
-    src[0].at = unit_parts(pl.chunk, static_cast<int64_t>(unit) * pu.n, pu.n, unit);
+    src[0].at = unit_parts(pl.chunk, static_cast<int64_t>(unit) * prefix_steps(g, pu) + g.unit_cost,
+                           pu.n, unit);
     src[0].rows = p.rp;
     src[0].r = (a - pb * g.qt_pre) * g.group + h;
   }
   const int32_t qb = tok / g.qt_seq, y = b * g.nqb + qb;
   bool dummy = false;
   int64_t before = 0;
-  for (int32_t yy = lane; yy < y; yy += 32) before += pair_tiles(g, yy, dummy);
+  for (int32_t yy = lane; yy < y; yy += 32) before += pair_steps(g, yy, dummy);
   before = warp_sum64(before) * g.n_kv_heads;
-  const int32_t n = pair_tiles(g, y, dummy);
-  src[1].at = unit_parts(pl.chunk, pl.prefix_all + before + static_cast<int64_t>(x) * n, n,
-                         y * g.n_kv_heads + x);
+  const int32_t steps = pair_steps(g, y, dummy);
+  src[1].at = unit_parts(
+      pl.chunk, pl.prefix_all + before + static_cast<int64_t>(x) * steps + g.unit_cost,
+      steps - g.unit_cost, y * g.n_kv_heads + x);
   src[1].rows = p.rs;
   src[1].r = (tok - qb * g.qt_seq) * g.group + h;
   grid_launch_dependents();

@@ -32,6 +32,7 @@ struct RowsGeom {
   int32_t prefix_rows;        // rows of the prefix tensors
   int32_t qt_seq, nqb;        // tokens per block of a sequence, blocks per sequence
   int32_t qt_pre, npb;        // (token, sequence) pairs per prefix block, blocks
+  int32_t unit_cost;          // what a unit costs besides its tiles, in tiles
 };
 
 GDATTN_HD int32_t imin32(int32_t a, int32_t b) { return a < b ? a : b; }

@@ -114,6 +114,7 @@ void check_case(std::mt19937_64 &rng, int k) {
   const int32_t pairs = g.batch * g.tokens;
   g.qt_pre = std::min(pairs, per_block);
   g.npb = (pairs + g.qt_pre - 1) / g.qt_pre;
+  g.unit_cost = pick(0, 4);
   const int32_t workers = pick(0, 2) ? pick(1, 20) : 148;
 
   // Rows against their units' tiles.
@@ -149,33 +150,35 @@ void check_case(std::mt19937_64 &rng, int k) {
   std::map<std::pair<bool, int32_t>, std::vector<std::pair<int32_t, int32_t>>> pieces;
   std::map<std::pair<bool, int64_t>, std::pair<std::pair<bool, int32_t>, int32_t>> slots;
   std::map<std::pair<bool, int32_t>, RowSegment> unit_of;
-  std::map<std::pair<bool, int32_t>, int64_t> unit_start;
-  int64_t at = 0;
   RowsPlan pl = {};
   std::vector<RowSegment> first_of(workers + 1);
   std::vector<bool> has_first(workers + 1, false);
-  std::vector<int64_t> cs(workers + 1, 0);
+  int64_t steps_done = 0;
   for (int32_t c = 0; c < workers; ++c) {
     pl = plan_of(g, c, workers);
     if (expect_bad && !pl.bad) fail("impossible lengths went unnoticed", k);
-    if (pl.cs != std::min(at, pl.total)) fail("chunks do not follow one another", k);
+    if (pl.cs != steps_done) fail("chunks do not follow one another", k);
     if (pl.ce - pl.cs > pl.chunk) fail("chunk too long", k);
-    cs[c] = pl.cs;
+    steps_done = pl.ce;
     RowSegments it;
     it.init(g, pl);
     RowSegment s;
+    int64_t last = -1;
+    int segments = 0;
     while (it.next(g, s)) {
-      if (s.opens != (at == pl.cs)) fail("opens", k);
-      if (s.opens) {
+      if (s.t0 < 0 || s.t1 <= s.t0 || s.t1 > s.u.n) fail("segment range", k);
+      const int64_t from = s.start + g.unit_cost + s.t0, to = s.start + g.unit_cost + s.t1;
+      if (from < pl.cs || to > pl.ce || from <= last) fail("a segment outside its chunk", k);
+      last = from;
+      if (s.opens != (segments == 0)) fail("opens", k);
+      if (segments++ == 0) {
         first_of[c] = s;
         has_first[c] = true;
       }
-      if (s.t0 < 0 || s.t1 <= s.t0 || s.t1 > s.u.n) fail("segment range", k);
       const std::pair<bool, int32_t> id(s.prefix, s.unit);
       pieces[id].emplace_back(s.t0, s.t1);
+      if (unit_of.count(id) && unit_of[id].start != s.start) fail("a unit's start moves", k);
       unit_of[id] = s;
-      if (s.t0 == 0) unit_start[id] = at;
-      at += s.t1 - s.t0;
       if (with_prefix || !s.whole()) {
         const int64_t slot = partial_slot(with_prefix, c, s.unit, s.opens);
         const int64_t units = s.prefix ? static_cast<int64_t>(g.npb) * g.n_kv_heads
@@ -186,9 +189,8 @@ void check_case(std::mt19937_64 &rng, int k) {
           fail("two partials in one slot", k);
       }
     }
-    if (at != pl.ce) fail("a chunk's segments do not fill it", k);
   }
-  if (at != pl.total) fail("tiles left out", k);
+  if (steps_done != pl.total) fail("steps left out", k);
   // (no windows: the unit covers [lo, P) with lo from the batch's shortest sequence)
   const UnitTiles pu = prefix_unit(g, P, pl.least_own);
   if (with_prefix) {
@@ -222,14 +224,14 @@ void check_case(std::mt19937_64 &rng, int k) {
   };
   if (with_prefix) {
     for (const auto &e : pieces)
-      expect_parts(e.first, unit_parts(pl.chunk, unit_start[e.first], unit_of[e.first].u.n,
-                                       e.first.second));
+      expect_parts(e.first, unit_parts(pl.chunk, unit_of[e.first].start + g.unit_cost,
+                                       unit_of[e.first].u.n, e.first.second));
   } else {
     for (int32_t c = 0; c + 1 < workers; ++c) {
       if (!has_first[c + 1]) continue;
       const RowSegment &s = first_of[c + 1];
       PartSlots ps;
-      if (cut_parts(pl.chunk, c, cs[c + 1], s.t0, s.u.n, ps)) {
+      if (cut_parts(pl.chunk, c, s.start, g.unit_cost, s.u.n, ps)) {
         const std::pair<bool, int32_t> id(false, s.unit);
         if (merged.count(id)) fail("a unit is merged twice", k);
         expect_parts(id, ps);

@@ -57,7 +57,10 @@ def test_row_planner(tmp_path):
      "static_cast<int64_t>(P) + least_own + 2 - g.window"),
     ("if (imax32(lo, g.sinks) < oldest) {", "if (lo < oldest - 2 * g.capacity - 100000) {"),
     (": 2 * static_cast<int64_t>(c) + (opens ? 0 : 1);", ": 2 * static_cast<int64_t>(c);"),
-    ("if (t0 == 0 || t0 > chunk) return false;", "if (t0 == 0) return false;"),
+    ("if (first < chunk * c) return false;", "if (first < 0) return false;"),
+    ("s.first = partial_slot(false, c, 0, start <= chunk * c);",
+     "s.first = partial_slot(false, c, 0, first <= chunk * c);"),
+    ("s.opens = s.start <= cs;", "s.opens = s.start < cs;"),
     ("if (y_start + span > pos) break;", "if (y_start + span >= pos) break;"),
 ])
 def test_planted_mistake_is_caught(tmp_path, original, planted):
