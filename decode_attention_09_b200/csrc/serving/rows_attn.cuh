@@ -87,6 +87,9 @@ struct RowsParams {
   float *lse;          // [T][B][Hq] or null
   float *own_o, *own_lse;  // partials of own units, rs rows a slot
   float *pre_o, *pre_lse;  // partials of prefix units, rp rows a slot
+  CutEntry *cuts;          // [workers - 1], a call without a prefix
+  PrefixEntry *prefix_entry;  // a call with one, and
+  int64_t *pair_start;        // [batch * nqb + 1]
   uint32_t *status;
   int32_t workers;
   int32_t rs, rp;      // rows of a slot
@@ -213,7 +216,25 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   if (warp == 0) {
     // --------------------------------------------------------- tile loads
     grid_dependency_wait();
-    if (plan.bad && worker == 0 && rank == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
+    if (rank == 0) {
+      if (plan.bad && worker == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
+      if (g.prefix_len != nullptr) {
+        if (worker == 0) write_pair_starts(g, plan, p.prefix_entry, p.pair_start);
+      } else if (worker > 0 && lane == 0) {
+        RowSegments it = segs;
+        CutEntry cut = {};
+        if (it.next(g, seg) &&
+            cut_parts(plan.chunk, worker - 1, seg.start, g.unit_cost, seg.u.n, cut.parts)) {
+          cut.b = seg.b;
+          cut.qb = seg.qb;
+          cut.x = seg.x;
+        } else {
+          cut.parts.n = 0;
+        }
+        p.cuts[worker - 1] = cut;
+      }
+      __syncwarp();
+    }
     const uint64_t pol = l2_evict_first_policy();
     bool ok = true;
     uint32_t nk = 0, nv = 0;  // tiles whose K, V were loaded
@@ -647,7 +668,8 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         const int64_t orow =
             (static_cast<int64_t>(tok) * g.batch + b) * Hq + seg.x * g.group + h;
         const int64_t prow =
-            partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens) *
+            static_cast<int64_t>(
+                partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens)) *
                 (seg.prefix ? p.rp : p.rs) + r;
         uint8_t *base =
             final_rows

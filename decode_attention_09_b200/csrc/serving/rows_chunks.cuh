@@ -185,15 +185,13 @@ struct RowSegments {
 // touching unit u of its kind writes slot c + u (if a later chunk touches unit u',
 // then u' >= u, so no two pieces share a slot).  Without one only pieces of split
 // units do, at most two a chunk: its first segment and its last.
-GDATTN_HD int64_t partial_slot(bool prefix_call, int32_t c, int32_t unit, bool opens) {
-  return prefix_call ? static_cast<int64_t>(c) + unit
-                     : 2 * static_cast<int64_t>(c) + (opens ? 0 : 1);
+GDATTN_HD int32_t partial_slot(bool prefix_call, int32_t c, int32_t unit, bool opens) {
+  return prefix_call ? c + unit : 2 * c + (opens ? 0 : 1);
 }
 
 // The slots of a unit's pieces: the first one's, then next, next + step, ...
 struct PartSlots {
-  int64_t first, next, step;
-  int32_t n;
+  int32_t first, next, step, n;
 };
 
 // Call with a prefix: a unit of its kind whose n > 0 tiles start at step `first`.
@@ -220,6 +218,50 @@ GDATTN_HD bool cut_parts(int64_t chunk, int32_t c, int64_t start, int32_t unit_c
   s.next = partial_slot(false, c + 1, 0, true);
   s.step = 2;
   return true;
+}
+
+// What the row kernel leaves for the merge, so that the merge plans nothing again (its
+// many CTAs doing so took 40 us behind an 8192-token prompt).
+// Without a prefix: entry c, written by worker c + 1, says whether the boundary behind
+// chunk c is a unit's first one (parts.n > 0), which unit and where its pieces are.
+struct CutEntry {
+  PartSlots parts;
+  int32_t b, qb, x, pad;
+};
+// With a prefix, written by worker 0: the chunk, a prefix unit's steps and tiles and the
+// first steps of the own pairs.
+struct PrefixEntry {
+  int64_t chunk;
+  int32_t prefix_steps, prefix_tiles;
+};
+
+// Run by one whole warp, for worker 0 of a call with a prefix.
+__device__ __forceinline__ void write_pair_starts(const RowsGeom &g, const RowsPlan &p,
+                                                  PrefixEntry *entry, int64_t *pair_start) {
+  const int lane = threadIdx.x & 31;
+  const int32_t pairs = g.batch * g.nqb;
+  if (lane == 0) {
+    const UnitTiles pu = prefix_unit(g, p.prefix_len, p.least_own);
+    entry->chunk = p.chunk;
+    entry->prefix_steps = prefix_steps(g, pu);
+    entry->prefix_tiles = pu.n;
+  }
+  int64_t base = p.prefix_all;
+  for (int32_t y0 = 0; y0 < pairs; y0 += 32) {
+    const int32_t y = y0 + lane;
+    bool dummy = false;
+    const int64_t span =
+        y < pairs ? static_cast<int64_t>(pair_steps(g, y, dummy)) * g.n_kv_heads : 0;
+    int64_t incl = span;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (y < pairs) pair_start[y] = base + incl - span;
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) pair_start[pairs] = base;
 }
 
 }  // namespace gdattn

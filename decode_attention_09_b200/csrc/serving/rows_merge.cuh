@@ -3,8 +3,8 @@
 // One to eight warps share an output row (more where there are few rows, whose parts
 // would otherwise be read one after the other: 64 rows of 65 parts at head_dim 512 took
 // 36 us with one warp a row), a lane owning D / 32 of its dims, sixteen 16-byte loads
-// in flight.  Where the parts are is worked out from the lengths before the wait on the
-// kernel in front.  Bound by latency: a few L2 round trips.
+// in flight.  The row kernel says where the parts are.  Bound by latency: a few L2 round
+// trips.
 #pragma once
 
 #include <cstdint>
@@ -21,7 +21,7 @@ struct RowParts {
   PartSlots at;
   int32_t rows, r;
   __device__ __forceinline__ int64_t row(int32_t i) const {
-    return (i == 0 ? at.first : at.next + (i - 1) * at.step) * rows + r;
+    return static_cast<int64_t>(i == 0 ? at.first : at.next + (i - 1) * at.step) * rows + r;
   }
 };
 
@@ -138,31 +138,26 @@ __device__ __forceinline__ void merge_row(const RowParts (&src)[2], bool real, i
   if (lane == 0 && lse != nullptr) *lse = s.z > 0.f ? (s.m + log2f(s.z)) * kLn2 : -INFINITY;
 }
 
-// Sinks: units that a chunk boundary cuts.  CTA x looks at the boundary behind
-// chunk x and joins the unit there if this is the unit's first boundary.
+// Sinks: units that a chunk boundary cuts.  CTA x joins the unit whose first boundary
+// is the one behind chunk x, if there is one.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_cut_units_kernel(const RowsParams p) {
   const RowsGeom &g = p.g;
-  const int32_t c = blockIdx.x;
-  const RowsPlan pl = plan_rows(g, c + 1, p.workers);  // every warp: no exchange needed
-  RowSegments segs;
-  segs.init(g, pl);
-  RowSegment seg;
-  RowParts src[2] = {};
-  const bool cut =
-      segs.next(g, seg) && cut_parts(pl.chunk, c, seg.start, g.unit_cost, seg.u.n, src[0].at);
   grid_launch_dependents();
   grid_dependency_wait();
-  if (!cut) return;
-  const int32_t nrow = imin32(g.qt_seq, g.tokens - seg.qb * g.qt_seq) * g.group;
+  const CutEntry cut = p.cuts[blockIdx.x];
+  if (cut.parts.n == 0) return;
+  const int32_t nrow = imin32(g.qt_seq, g.tokens - cut.qb * g.qt_seq) * g.group;
   const int32_t r = blockIdx.y * (kMergeWarps / p.merge_shares) + (threadIdx.x >> 5) / p.merge_shares;
+  RowParts src[2] = {};
+  src[0].at = cut.parts;
   src[0].o = p.own_o;
   src[0].lse = p.own_lse;
   src[0].rows = p.rs;
   src[0].r = r;
   const int32_t tq = r / g.group, h = r - tq * g.group;
-  const int64_t row = (static_cast<int64_t>(seg.qb * g.qt_seq + tq) * g.batch + seg.b) *
-                          (g.n_kv_heads * g.group) + seg.x * g.group + h;
+  const int64_t row = (static_cast<int64_t>(cut.qb * g.qt_seq + tq) * g.batch + cut.b) *
+                          (g.n_kv_heads * g.group) + cut.x * g.group + h;
   merge_row<D>(src, r < nrow, p.merge_shares, p.out + row * D,
                p.lse != nullptr ? p.lse + row : nullptr);
 }
@@ -171,7 +166,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_cut_units_kernel(const Ro
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_prefix_kernel(const RowsParams p) {
   const RowsGeom &g = p.g;
-  const int lane = threadIdx.x & 31;
   const int32_t Hq = g.n_kv_heads * g.group;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeWarps / p.merge_shares) +
                       (threadIdx.x >> 5) / p.merge_shares;
@@ -180,34 +174,28 @@ __global__ void __launch_bounds__(kMergeThreads) merge_prefix_kernel(const RowsP
   const int32_t a = static_cast<int32_t>(safe / Hq), hq = static_cast<int32_t>(safe % Hq);
   const int32_t x = hq / g.group, h = hq - x * g.group;
   const int32_t tok = a / g.batch, b = a - tok * g.batch;
-  const RowsPlan pl = plan_rows(g, 0, p.workers);
-  const UnitTiles pu = prefix_unit(g, pl.prefix_len, pl.least_own);
+  const int32_t pb = a / g.qt_pre, qb = tok / g.qt_seq, y = b * g.nqb + qb;
   RowParts src[2] = {};
   src[0].o = p.pre_o;
   src[0].lse = p.pre_lse;
+  src[0].rows = p.rp;
+  src[0].r = (a - pb * g.qt_pre) * g.group + h;
   src[1].o = p.own_o;
   src[1].lse = p.own_lse;
-  if (pu.n > 0) {
-    const int32_t pb = a / g.qt_pre;
-    const int32_t unit = x * g.npb + pb;
-    src[0].at = unit_parts(pl.chunk, static_cast<int64_t>(unit) * prefix_steps(g, pu) + g.unit_cost,
-                           pu.n, unit);
-    src[0].rows = p.rp;
-    src[0].r = (a - pb * g.qt_pre) * g.group + h;
-  }
-  const int32_t qb = tok / g.qt_seq, y = b * g.nqb + qb;
-  bool dummy = false;
-  int64_t before = 0;
-  for (int32_t yy = lane; yy < y; yy += 32) before += pair_steps(g, yy, dummy);
-  before = warp_sum64(before) * g.n_kv_heads;
-  const int32_t steps = pair_steps(g, y, dummy);
-  src[1].at = unit_parts(
-      pl.chunk, pl.prefix_all + before + static_cast<int64_t>(x) * steps + g.unit_cost,
-      steps - g.unit_cost, y * g.n_kv_heads + x);
   src[1].rows = p.rs;
   src[1].r = (tok - qb * g.qt_seq) * g.group + h;
   grid_launch_dependents();
   grid_dependency_wait();
+  const PrefixEntry entry = *p.prefix_entry;
+  const int64_t start = p.pair_start[y];
+  const int32_t steps = static_cast<int32_t>((p.pair_start[y + 1] - start) / g.n_kv_heads);
+  if (entry.prefix_tiles > 0) {
+    const int32_t unit = x * g.npb + pb;
+    src[0].at = unit_parts(entry.chunk, static_cast<int64_t>(unit) * entry.prefix_steps + g.unit_cost,
+                           entry.prefix_tiles, unit);
+  }
+  src[1].at = unit_parts(entry.chunk, start + static_cast<int64_t>(x) * steps + g.unit_cost,
+                         steps - g.unit_cost, y * g.n_kv_heads + x);
   merge_row<D>(src, real, p.merge_shares, p.out + row * D,
                p.lse != nullptr ? p.lse + row : nullptr);
 }

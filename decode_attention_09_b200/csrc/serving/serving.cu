@@ -122,7 +122,7 @@ struct RowsLayout {
   RowsGeom g = {};
   int nh = 1, workers = 0;
   int32_t rs = 0, rp = 0;
-  size_t own_o = 0, own_lse = 0, pre_o = 0, pre_lse = 0, bytes = 0;
+  size_t table = 0, own_o = 0, own_lse = 0, pre_o = 0, pre_lse = 0, bytes = 0;
 };
 
 // Blocks, workers and workspace of a call (prefix_rows 0: a call without a prefix).
@@ -157,9 +157,15 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
   const int64_t own_slots = prefix_rows > 0 ? lay.workers + own_units : 2 * lay.workers;
   const int64_t pre_slots =
       prefix_rows > 0 ? lay.workers + static_cast<int64_t>(g.npb) * g.n_kv_heads : 0;
+  if (own_slots > INT32_MAX || pre_slots > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
   const size_t own_rows = static_cast<size_t>(own_slots) * lay.rs;
   const size_t pre_rows = static_cast<size_t>(pre_slots) * lay.rp;
-  lay.own_lse = kHeaderBytes;
+  // Behind the header: what the row kernel tells the merge.
+  lay.table = kHeaderBytes;
+  const size_t table_bytes =
+      prefix_rows > 0 ? 256 + (static_cast<size_t>(batch) * g.nqb + 1) * sizeof(int64_t)
+                      : static_cast<size_t>(lay.workers) * sizeof(CutEntry);
+  lay.own_lse = align256(lay.table + table_bytes);
   lay.pre_lse = align256(lay.own_lse + own_rows * 4);
   lay.own_o = align256(lay.pre_lse + pre_rows * 4);
   lay.pre_o = align256(lay.own_o + own_rows * d->head_dim * 4);
@@ -226,6 +232,9 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   p.own_lse = reinterpret_cast<float *>(ws + lay.own_lse);
   p.pre_o = reinterpret_cast<float *>(ws + lay.pre_o);
   p.pre_lse = reinterpret_cast<float *>(ws + lay.pre_lse);
+  p.cuts = reinterpret_cast<CutEntry *>(ws + lay.table);
+  p.prefix_entry = reinterpret_cast<PrefixEntry *>(ws + lay.table);
+  p.pair_start = reinterpret_cast<int64_t *>(ws + lay.table + 256);
   p.status = reinterpret_cast<uint32_t *>(ws);
   p.workers = lay.workers;
   p.rs = lay.rs;

@@ -56,7 +56,8 @@ def test_row_planner(tmp_path):
     ("static_cast<int64_t>(P) + least_own + 1 - g.window",
      "static_cast<int64_t>(P) + least_own + 2 - g.window"),
     ("if (imax32(lo, g.sinks) < oldest) {", "if (lo < oldest - 2 * g.capacity - 100000) {"),
-    (": 2 * static_cast<int64_t>(c) + (opens ? 0 : 1);", ": 2 * static_cast<int64_t>(c);"),
+    ("return prefix_call ? c + unit : 2 * c + (opens ? 0 : 1);",
+     "return prefix_call ? c + unit : 2 * c;"),
     ("if (first < chunk * c) return false;", "if (first < 0) return false;"),
     ("s.first = partial_slot(false, c, 0, start <= chunk * c);",
      "s.first = partial_slot(false, c, 0, first <= chunk * c);"),
