@@ -492,15 +492,14 @@ def read_probe(src: torch.Tensor, mode: int, sink: torch.Tensor, stream=None) ->
 # These wrappers are called once per layer and step, so what they cost the host counts:
 # an argument is first tested as a whole (``_fits``), and only one that fails goes
 # through the checks that name what is wrong with it.
-def _call(fn, what: str, device, stream, *args) -> None:
-    """fn(*args, stream) with ``device`` current: the library launches on the current
-    device, so a call follows its tensors.  stream None: the device's current one."""
-    index = device.index
-    if index is not None and index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(fn, what, device, stream, *args)
+def _call(fn, what: str, index: int, stream, *args) -> None:
+    """fn(*args, stream) with device ``index`` current: the library launches on the
+    current device, so a call follows its tensors.  stream None: the device's current one."""
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _call(fn, what, index, stream, *args)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(-1 if index is None else index)
+        stream = torch._C._cuda_getCurrentRawStream(index)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     st = fn(*args, stream)
@@ -508,50 +507,55 @@ def _call(fn, what: str, device, stream, *args) -> None:
         raise GdattnError(st, what)
 
 
-def _fits(t: torch.Tensor, dtype, numel: int, device) -> bool:
-    return (t.dtype is dtype and t.device == device and t.is_contiguous()
+def _fits(t: torch.Tensor, dtype, numel: int, index: int) -> bool:
+    return (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
             and t.numel() >= numel)
 
 
-def _need(t: torch.Tensor, name: str, dtype, numel: int, device) -> None:
-    if not _fits(t, dtype, numel, device):
-        _dense(t, name, (dtype,), numel, device)
+def _need(t: torch.Tensor, name: str, dtype, numel: int, like: torch.Tensor, index: int) -> None:
+    """A dense argument on the device of ``like``, which is device ``index``."""
+    if not _fits(t, dtype, numel, index):
+        _dense(t, name, (dtype,), numel, like.device)
 
 
-def _need_cache(t: torch.Tensor, name: str, dtypes, numel: int, device) -> None:
-    if not _fits(t, dtypes[0], numel, device):  # dense caches; strided ones reach further
-        _extent(t, name, dtypes, numel, device)
+def _need_cache(t: torch.Tensor, name: str, dtypes, numel: int, like: torch.Tensor,
+                index: int) -> None:
+    if not _fits(t, dtypes[0], numel, index):  # dense caches; strided ones reach further
+        _extent(t, name, dtypes, numel, like.device)
+
+
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _check_tokens(q, k, v, seqlens, out, lse, desc):
     """The arguments both continuous-batching attention calls share: q and out bf16
     [T, B, Hq, D], lse fp32 [T, B, Hq] or None, caches spanning B sequences.  Returns
-    (T, B, device, out, lse), with out and lse allocated where they are None."""
+    (T, B, device index, out, lse), with out and lse allocated where they are None."""
     T, B, Hq, D = q.shape
-    device = q.device
+    index = q.get_device()
     if Hq != desc.n_q_heads or D != desc.head_dim:
         raise ValueError(f"q: heads and head_dim {(Hq, D)}, the descriptor has "
                          f"{(int(desc.n_q_heads), int(desc.head_dim))}")
-    if q.dtype is not torch.bfloat16 or not q.is_contiguous() or not q.is_cuda:
-        _dense(q, "q", _BF16, q.numel(), device)
+    if index < 0 or q.dtype is not _bf16 or not q.is_contiguous():
+        _dense(q, "q", _BF16, q.numel(), q.device)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need(out, "out", torch.bfloat16, T * B * Hq * D, device)
+        _need(out, "out", _bf16, T * B * Hq * D, q, index)
     if lse is None:
-        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=device)
+        lse = q.new_empty((T, B, Hq), dtype=_f32)
     else:
-        _need(lse, "lse", torch.float32, T * B * Hq, device)
+        _need(lse, "lse", _f32, T * B * Hq, q, index)
     n = _cache_elems(B, desc)
-    _need_cache(k, "k", _BF16, n, device)
+    _need_cache(k, "k", _BF16, n, q, index)
     if v is not None:
-        _need_cache(v, "v", _BF16, n, device)
-    _need(seqlens, "seqlens", torch.int32, B, device)
-    return T, B, device, out, lse
+        _need_cache(v, "v", _BF16, n, q, index)
+    _need(seqlens, "seqlens", _i32, B, q, index)
+    return T, B, index, out, lse
 
 
-def _check_workspace(workspace, device) -> None:
-    _need(workspace, "workspace", torch.uint8, 0, device)
+def _check_workspace(workspace, like, index: int) -> None:
+    _need(workspace, "workspace", _u8, 0, like, index)
 
 
 def sink_workspace_size(batch: int, n_tokens: int, max_seqlen: int, desc: LayerDesc,
@@ -608,11 +612,11 @@ def decode_sink(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
     """Sliding-window attention with n_sink pinned first tokens through
     gdattn_decode_sink.  q bf16 [T, B, Hq, D]: token t of sequence b at position
     L_b - T + t.  Returns (out, lse), token-major."""
-    T, B, device, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
+    T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
     if workspace is None:
-        workspace = alloc_sink_workspace(B, T, max_seqlen, desc, n_sink, device, stream)
-    _check_workspace(workspace, device)
-    _call(lib().gdattn_decode_sink, "gdattn_decode_sink", device, stream, q.data_ptr(),
+        workspace = alloc_sink_workspace(B, T, max_seqlen, desc, n_sink, q.device, stream)
+    _check_workspace(workspace, q, index)
+    _call(lib().gdattn_decode_sink, "gdattn_decode_sink", index, stream, q.data_ptr(),
           k.data_ptr(), _ptr(v), seqlens.data_ptr(), B, T, max_seqlen, ctypes.byref(desc), n_sink,
           out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse
@@ -638,17 +642,17 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: Optional[to
     q bf16 [T, B, Hq, D]; k_prefix / v_prefix bf16 [prefix_rows, Hkv, D] (v_prefix None
     when K = V); prefix_len int32 [1] on the device; k, v, seqlens the sequences' own
     caches and lengths.  Returns (out, lse), token-major."""
-    T, B, device, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
+    T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
     rows = k_prefix.shape[0]
     n = rows * desc.n_kv_heads * desc.head_dim
-    _need(k_prefix, "k_prefix", torch.bfloat16, n, device)
+    _need(k_prefix, "k_prefix", _bf16, n, q, index)
     if v_prefix is not None:
-        _need(v_prefix, "v_prefix", torch.bfloat16, n, device)
-    _need(prefix_len, "prefix_len", torch.int32, 1, device)
+        _need(v_prefix, "v_prefix", _bf16, n, q, index)
+    _need(prefix_len, "prefix_len", _i32, 1, q, index)
     if workspace is None:
-        workspace = alloc_prefix_workspace(B, T, max_seqlen, rows, desc, device, stream)
-    _check_workspace(workspace, device)
-    _call(lib().gdattn_decode_prefix, "gdattn_decode_prefix", device, stream, q.data_ptr(),
+        workspace = alloc_prefix_workspace(B, T, max_seqlen, rows, desc, q.device, stream)
+    _check_workspace(workspace, q, index)
+    _call(lib().gdattn_decode_prefix, "gdattn_decode_prefix", index, stream, q.data_ptr(),
           k_prefix.data_ptr(), _ptr(v_prefix), prefix_len.data_ptr(), rows, k.data_ptr(), _ptr(v),
           seqlens.data_ptr(), B, T, max_seqlen, ctypes.byref(desc), out.data_ptr(),
           lse.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -668,56 +672,59 @@ def slot_map(seqlens: torch.Tensor, new_lens: torch.Tensor, n_rows: int, capacit
              n_sink: int = 0, out: Optional[RowMap] = None, stream=None) -> RowMap:
     """gdattn_slot_map: the slots of a step in which new_lens[b] tokens join sequence
     b (seqlens[b] long with them), packed into n_rows rows."""
-    B, device = seqlens.numel(), seqlens.device
-    _need(seqlens, "seqlens", torch.int32, B, device)
-    _need(new_lens, "new_lens", torch.int32, B, device)
-    _on(seqlens, "seqlens", device)
+    B, index = seqlens.numel(), seqlens.get_device()
+    _need(seqlens, "seqlens", _i32, B, seqlens, index)
+    _need(new_lens, "new_lens", _i32, B, seqlens, index)
+    if index < 0:
+        _on(seqlens, "seqlens", None)
     if n_rows < 0:
         raise ValueError(f"n_rows: {n_rows}")
     if out is None:
-        flat = torch.empty(B + 1 + 3 * n_rows, dtype=torch.int32, device=device)
+        flat = seqlens.new_empty(B + 1 + 3 * n_rows)
         out = RowMap(*flat.split_with_sizes((B + 1, n_rows, n_rows, n_rows)))
         start = flat.data_ptr()
         seq = start + 4 * (B + 1)
         pos, slot = seq + 4 * n_rows, seq + 8 * n_rows
     else:
-        _need(out.start, "out.start", torch.int32, B + 1, device)
+        _need(out.start, "out.start", _i32, B + 1, seqlens, index)
         for name in ("seq", "pos", "slot"):
-            _need(getattr(out, name), f"out.{name}", torch.int32, n_rows, device)
+            _need(getattr(out, name), f"out.{name}", _i32, n_rows, seqlens, index)
         start, seq, pos, slot = (t.data_ptr() for t in out)
-    _call(lib().gdattn_slot_map, "gdattn_slot_map", device, stream, seqlens.data_ptr(),
+    _call(lib().gdattn_slot_map, "gdattn_slot_map", index, stream, seqlens.data_ptr(),
           new_lens.data_ptr(), B, n_rows, capacity, n_sink, start, seq, pos, slot)
     return out
 
 
-def _row_stride(rows: torch.Tensor, name: str, desc: LayerDesc, n_rows: int, device) -> int:
+def _row_stride(rows: torch.Tensor, name: str, desc: LayerDesc, n_rows: int, like,
+                index: int) -> int:
     """Elements between the rows of a bf16 [n_rows, Hkv, D] tensor whose heads are
     next to one another (a slice of a fused projection is)."""
     H, D = desc.n_kv_heads, desc.head_dim
-    if rows.dtype is not torch.bfloat16:
+    if rows.dtype is not _bf16:
         raise ValueError(f"{name}: dtype {rows.dtype}, expected torch.bfloat16")
     if rows.dim() != 3 or rows.shape[0] < n_rows or rows.shape[1] != H or rows.shape[2] != D:
         raise ValueError(f"{name}: shape {tuple(rows.shape)}, expected at least {(n_rows, H, D)}")
     stride = rows.stride()
     if stride[2] != 1 or (H > 1 and stride[1] != D):
         raise ValueError(f"{name}: the heads of a row must be next to one another")
-    _on(rows, name, device)
+    if index < 0 or rows.get_device() != index:
+        _on(rows, name, like.device)
     return stride[0] if rows.shape[0] > 1 else H * D
 
 
 def _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, dtypes):
     """The arguments both cache writes share; returns (n_rows, batch, row stride)."""
-    device = k.device
+    index = k.get_device()
     n_rows, batch = row_slot.numel(), k.shape[0]
-    _need(row_seq, "row_seq", torch.int32, n_rows, device)
-    _need(row_slot, "row_slot", torch.int32, n_rows, device)
-    stride = _row_stride(k_rows, "k_rows", desc, n_rows, device)
+    _need(row_seq, "row_seq", _i32, n_rows, k, index)
+    _need(row_slot, "row_slot", _i32, n_rows, k, index)
+    stride = _row_stride(k_rows, "k_rows", desc, n_rows, k, index)
     n = _cache_elems(batch, desc)
-    _need_cache(k, "k", dtypes, n, device)
-    if v_rows is not None and _row_stride(v_rows, "v_rows", desc, n_rows, device) != stride:
+    _need_cache(k, "k", dtypes, n, k, index)
+    if v_rows is not None and _row_stride(v_rows, "v_rows", desc, n_rows, k, index) != stride:
         raise ValueError("v_rows: must have the row stride of k_rows")
     if v is not None:
-        _need_cache(v, "v", dtypes, n, device)
+        _need_cache(v, "v", dtypes, n, k, index)
     return n_rows, batch, stride
 
 
@@ -734,7 +741,7 @@ def cache_write(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_seq: t
     """gdattn_cache_write: rows bf16 [n_rows, Hkv, D] (any row stride) into the caches
     k, v [B, C, Hkv, D] by a slot map; v_rows and v None when K = V."""
     n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, _BF16)
-    _call(lib().gdattn_cache_write, "gdattn_cache_write", k.device, stream, k_rows.data_ptr(),
+    _call(lib().gdattn_cache_write, "gdattn_cache_write", k.get_device(), stream, k_rows.data_ptr(),
           _ptr(v_rows), stride, row_seq.data_ptr(), row_slot.data_ptr(), n_rows, batch,
           ctypes.byref(desc), k.data_ptr(), _ptr(v))
 
@@ -755,12 +762,12 @@ def cache_write_fp8(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_se
     float8_e4m3fn) and their scales, fp32 [B, Hkv, C]."""
     n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k_codes,
                                          v_codes, _CODES)
-    device = k_codes.device
+    index = k_codes.get_device()
     scales = batch * desc.n_kv_heads * desc.cache_capacity
-    _need(k_scale, "k_scale", torch.float32, scales, device)
+    _need(k_scale, "k_scale", _f32, scales, k_codes, index)
     if v_scale is not None:
-        _need(v_scale, "v_scale", torch.float32, scales, device)
-    _call(lib().gdattn_cache_write_fp8, "gdattn_cache_write_fp8", device, stream,
+        _need(v_scale, "v_scale", _f32, scales, k_codes, index)
+    _call(lib().gdattn_cache_write_fp8, "gdattn_cache_write_fp8", index, stream,
           k_rows.data_ptr(), _ptr(v_rows), stride, row_seq.data_ptr(), row_slot.data_ptr(),
           n_rows, batch, ctypes.byref(desc), k_codes.data_ptr(), _ptr(v_codes),
           k_scale.data_ptr(), _ptr(v_scale))

@@ -183,76 +183,80 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 // normal, for every quotient that is not far below e4m3's smallest number.
 __device__ __forceinline__ bool plain_scale(float s) { return s > 1e-18f && s < 1e30f; }
 
-// Word w of four (w a constant), two bf16.
-__device__ __forceinline__ uint32_t word(const uint4 &v, int w) {
-  return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7FFF7FFFu));
+  return r;
 }
 
-// One warp per (row, KV head) at a time, kFp8Rows of them in flight: the row's largest
-// magnitude, then its codes.  Bound by HBM (2 D bytes read, D + 4 written).
-constexpr int kFp8Rows = 4;
+__device__ __forceinline__ uint32_t codes_of(uint32_t x, uint32_t y, float s, float r) {
+  return e4m3x2_rn(quotient(bf16lo(x), s, r), quotient(bf16hi(x), s, r)) |
+         static_cast<uint32_t>(e4m3x2_rn(quotient(bf16lo(y), s, r), quotient(bf16hi(y), s, r)))
+             << 16;
+}
+__device__ __forceinline__ uint32_t codes_by_division(uint32_t x, uint32_t y, float s) {
+  if (!(s > 0.f)) return 0;  // a row of zeros
+  return e4m3x2_rn(__fdiv_rn(bf16lo(x), s), __fdiv_rn(bf16hi(x), s)) |
+         static_cast<uint32_t>(e4m3x2_rn(__fdiv_rn(bf16lo(y), s), __fdiv_rn(bf16hi(y), s))) << 16;
+}
+
+// A row of one KV head: its largest magnitude, then its codes.  D / 32 lanes share a
+// row, 32 elements each, so that what a row costs besides its elements is spread over
+// four (D = 256) rows a warp: with a warp for each row the kernel was bound by
+// instructions (51 us for 12000 rows of 8 heads; this way HBM bounds it, 2 D bytes
+// read and D + 4 written).
 template <int D>
 __global__ void __launch_bounds__(kCacheWriteThreads)
     cache_write_fp8_kernel(const CacheWriteParams p) {
-  constexpr int E = D / 32;  // elements per lane: 8 or 16
-  const int lane = threadIdx.x & 31;
+  constexpr int LANES = D / 32;              // of a row
+  constexpr int ROWS = kCacheWriteThreads / LANES;
+  const int l = threadIdx.x % LANES;
   const uint16_t *rows = blockIdx.y == 0 ? p.k_rows : p.v_rows;
   uint8_t *cache = blockIdx.y == 0 ? p.k_cache : p.v_cache;
   float *scales = blockIdx.y == 0 ? p.k_scale : p.v_scale;
   const uint32_t H = static_cast<uint32_t>(p.n_kv_heads);
   const int64_t row_elems = static_cast<int64_t>(H) * D;
-  const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * (kCacheWriteThreads / 32) + (threadIdx.x >> 5)) * kFp8Rows;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS;
   const int64_t r0 = first / H;
-  const uint32_t h0 = static_cast<uint32_t>(first - r0 * H);
-  uint4 raw[kFp8Rows][E / 8];
-  int64_t dst[kFp8Rows], sat[kFp8Rows];
+  const uint32_t hh = static_cast<uint32_t>(first - r0 * H) + threadIdx.x / LANES;
+  const uint32_t row = hh / H, h = hh - row * H;
+  const int64_t r = r0 + row;
+  int32_t b = 0, slot = 0;
+  const bool there = r < p.n_rows && row_target(p, static_cast<int32_t>(r), b, slot);
+  uint4 x[4] = {};
+  if (there) {
+    const uint16_t *src = rows + r * p.row_stride + h * D + l * 8;
 #pragma unroll
-  for (int j = 0; j < kFp8Rows; ++j) {
-    const uint32_t row = (h0 + j) / H, h = h0 + j - row * H;
-    const int64_t r = r0 + row;
-    dst[j] = -1;
-    int32_t b, slot;
-    if (r < p.n_rows && row_target(p, static_cast<int32_t>(r), b, slot)) {
-      dst[j] = b * p.batch_stride + slot * row_elems + h * D + lane * E;
-      sat[j] = (static_cast<int64_t>(b) * H + h) * p.capacity + slot;
-      const uint16_t *src = rows + r * p.row_stride + h * D + lane * E;
-#pragma unroll
-      for (int c = 0; c < E / 8; ++c) raw[j][c] = ld_nc_v4(src + 8 * c);
-    }
+    for (int c = 0; c < 4; ++c) x[c] = ld_nc_v4(src + c * 8 * LANES);
   }
+  uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < kFp8Rows; ++j) {
-    if (dst[j] < 0) continue;  // the whole warp
-    float amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < E / 2; ++c) {
-      const uint32_t x = word(raw[j][c / 4], c % 4);
-      amax = fmaxf(amax, fmaxf(fabsf(bf16lo(x)), fabsf(bf16hi(x))));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = __fdiv_rn(amax, 448.f);
-    const bool plain = plain_scale(scale);  // of the whole warp
-    const float inv = plain ? __frcp_rn(scale) : 0.f;
-    uint32_t code[E / 4] = {};
-#pragma unroll
-    for (int c = 0; c < E / 2; ++c) {
-      const uint32_t x = word(raw[j][c / 4], c % 4);
-      uint16_t two = 0;
-      if (plain)
-        two = e4m3x2_rn(quotient(bf16lo(x), scale, inv), quotient(bf16hi(x), scale, inv));
-      else if (scale > 0.f)
-        two = e4m3x2_rn(__fdiv_rn(bf16lo(x), scale), __fdiv_rn(bf16hi(x), scale));
-      code[c / 2] |= static_cast<uint32_t>(two) << (16 * (c % 2));
-    }
-    if (E == 8)
-      *reinterpret_cast<uint2 *>(cache + dst[j]) = make_uint2(code[0], code[1]);
-    else
-      *reinterpret_cast<uint4 *>(cache + dst[j]) =
-          make_uint4(code[0], code[1], code[E / 4 - 2], code[E / 4 - 1]);
-    if (lane == 0) scales[sat[j]] = scale;
+  for (int c = 0; c < 4; ++c) {
+    top = absmax_bf16x2(top, x[c].x);
+    top = absmax_bf16x2(top, x[c].y);
+    top = absmax_bf16x2(top, x[c].z);
+    top = absmax_bf16x2(top, x[c].w);
   }
+  float amax = fmaxf(bf16lo(top), bf16hi(top));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float scale = __fdiv_rn(amax, 448.f);
+  if (!there) return;
+  uint8_t *dst = cache + b * p.batch_stride + slot * row_elems + h * D + l * 8;
+  if (plain_scale(scale)) {
+    const float inv = __frcp_rn(scale);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint2 *>(dst + c * 8 * LANES) =
+          make_uint2(codes_of(x[c].x, x[c].y, scale, inv), codes_of(x[c].z, x[c].w, scale, inv));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint2 *>(dst + c * 8 * LANES) = make_uint2(
+          codes_by_division(x[c].x, x[c].y, scale), codes_by_division(x[c].z, x[c].w, scale));
+  }
+  if (l == 0) scales[(static_cast<int64_t>(b) * H + h) * p.capacity + slot] = scale;
 }
 
 }  // namespace gdattn

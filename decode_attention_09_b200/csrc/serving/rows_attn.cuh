@@ -24,8 +24,8 @@
 //
 // Work split: rows_chunks.cuh lays all tiles end to end and gives each worker (CTA
 // or pair) an equal chunk; loads run ahead across units.  Whole units are written
-// directly (sinks), pieces as normalised fp32 partials plus log2-sum-exp, which
-// rows_merge.cuh joins.
+// directly (sinks), pieces as normalised fp32 partials plus log2-sum-exp, which the
+// CTA of the last piece joins where a block has few rows, and rows_merge.cuh elsewhere.
 //
 // Shared memory (1 CTA per SM): Q blocks (64 KiB; two buffers when a block's rows
 // fill at most half), a ring of 32 KiB tiles (five for NH = 1; three for NH = 2 beside
@@ -87,9 +87,11 @@ struct RowsParams {
   float *lse;          // [T][B][Hq] or null
   float *own_o, *own_lse;  // partials of own units, rs rows a slot
   float *pre_o, *pre_lse;  // partials of prefix units, rp rows a slot
-  CutEntry *cuts;          // [workers - 1], a call without a prefix
+  CutEntry *cuts;          // [workers - 1], a call without a prefix (null: the last piece's
+                           // CTA joins a cut unit here, no merge kernel follows), and
+  uint32_t *counters;      // [workers * NH] pieces left so far, zero between calls
   PrefixEntry *prefix_entry;  // a call with one, and
-  int64_t *pair_start;        // [batch * nqb + 1]
+  int32_t *pair_start;        // [batch * nqb + 1]
   uint32_t *status;
   int32_t workers;
   int32_t rs, rp;      // rows of a slot
@@ -125,6 +127,59 @@ __device__ __forceinline__ uint32_t v_entry(uint32_t i) {
   return SHARED ? i : 2 * i + a + 1;
 }
 
+// Joins the pieces of one row of a cut unit, 256 dims of it, by one warp:
+//   lse = log2 sum_i 2^lse_i,  out = sum_i 2^(lse_i - lse) o_i.
+template <int D>
+__device__ __noinline__ void join_pieces(const float *o, const float *lse, const PartSlots &at,
+                                            int32_t rows, int32_t r, uint16_t *out,
+                                            float *out_lse) {
+  constexpr int kFlight = 4;
+  const int lane = threadIdx.x & 31;
+  float4 acc[2] = {};
+  float m = -INFINITY, z = 0.f;
+  for (int32_t i0 = 0; i0 < at.n; i0 += kFlight) {
+    float e[kFlight];
+    float4 v[kFlight][2];
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      const int32_t i = i0 + q;
+      e[q] = -INFINITY;
+      if (i < at.n) {
+        const int64_t row =
+            static_cast<int64_t>(i == 0 ? at.first : at.next + (i - 1) * at.step) * rows + r;
+        e[q] = __ldcg(lse + row);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          v[q][c] = __ldcg(reinterpret_cast<const float4 *>(o + row * D) + c * 32 + lane);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      if (e[q] == -INFINITY) continue;  // an empty piece adds nothing
+      const float top = fmaxf(m, e[q]);
+      const float a = exp2f(m - top), f = exp2f(e[q] - top);
+      m = top;
+      z = fmaf(z, a, f);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        acc[c].x = fmaf(f, v[q][c].x, acc[c].x * a);
+        acc[c].y = fmaf(f, v[q][c].y, acc[c].y * a);
+        acc[c].z = fmaf(f, v[q][c].z, acc[c].z * a);
+        acc[c].w = fmaf(f, v[q][c].w, acc[c].w * a);
+      }
+    }
+  }
+  const float inv = z > 0.f ? __fdividef(1.f, z) : 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint2 pk;
+    pk.x = pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
+    pk.y = pack_bf16x2(acc[c].z * inv, acc[c].w * inv);
+    *reinterpret_cast<uint2 *>(out + (c * 32 + lane) * 4) = pk;
+  }
+  if (lane == 0 && out_lse != nullptr) *out_lse = z > 0.f ? (m + log2f(z)) * kLn2 : -INFINITY;
+}
+
 template <int NH, bool SHARED, bool CAP>
 __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     rows_attn_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
@@ -156,6 +211,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 64);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 65);
   RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 66);
+  volatile int *last_piece = reinterpret_cast<volatile int *>(bars + 100);  // [2 groups]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -208,33 +264,16 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   if (NH == 2) cluster_sync();  // the peer's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_base_smem;
-  const RowsPlan plan = *plan_smem;
+  const RowsPlan &plan = *plan_smem;
   RowSegments segs;
   segs.init(g, plan);
   RowSegment seg;
 
   if (warp == 0) {
     // --------------------------------------------------------- tile loads
-    grid_dependency_wait();
-    if (rank == 0) {
-      if (plan.bad && worker == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
-      if (g.prefix_len != nullptr) {
-        if (worker == 0) write_pair_starts(g, plan, p.prefix_entry, p.pair_start);
-      } else if (worker > 0 && lane == 0) {
-        RowSegments it = segs;
-        CutEntry cut = {};
-        if (it.next(g, seg) &&
-            cut_parts(plan.chunk, worker - 1, seg.start, g.unit_cost, seg.u.n, cut.parts)) {
-          cut.b = seg.b;
-          cut.qb = seg.qb;
-          cut.x = seg.x;
-        } else {
-          cut.parts.n = 0;
-        }
-        p.cuts[worker - 1] = cut;
-      }
-      __syncwarp();
-    }
+    // Tiles without any of the step's own rows hold what earlier steps wrote and are
+    // loaded before the kernel in front has ended.
+    bool waited = false;
     const uint64_t pol = l2_evict_first_policy();
     bool ok = true;
     uint32_t nk = 0, nv = 0;  // tiles whose K, V were loaded
@@ -245,6 +284,10 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       if (e >= NST) ok = mbar_wait(&empty[st], ((e / NST) - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
+      if (!waited && !sg.prefix && tile.pos + tile.ntok > sg.L - g.tokens) {
+        grid_dependency_wait();
+        waited = true;
+      }
       uint64_t *bar = is_v ? &vfull[nv & 7] : &kfull[nk & 7];
       if (!(p.test_withhold && e == 0) && elect_one()) {
         const bool big = tile.ntok > 48;
@@ -300,6 +343,26 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q loads
     grid_dependency_wait();
+    if (rank == 0) {
+      if (plan.bad && worker == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
+      if (g.prefix_len != nullptr) {
+        if (worker == 0) write_pair_starts(g, plan, p.prefix_entry, p.pair_start);
+      } else if (p.cuts != nullptr && worker > 0 && lane == 0) {
+        RowSegments it = segs;
+        CutEntry cut = {};
+        if (it.next(g, seg) &&
+            cut_parts(plan.total, p.workers, worker - 1, seg.start, g.unit_cost, seg.u.n,
+                      cut.parts)) {
+          cut.b = seg.b;
+          cut.qb = seg.qb;
+          cut.x = seg.x;
+        } else {
+          cut.parts.n = 0;
+        }
+        p.cuts[worker - 1] = cut;
+      }
+      __syncwarp();
+    }
     bool ok = true;
     uint32_t n = 0;  // blocks so far
     while (ok && segs.next(g, seg)) {
@@ -471,13 +534,14 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // from tensor memory.
           if (ok) tc_fence_after();
           if (NH == 2) {
-            // The peer holds the scores' other half of the dims: swap and add.
+            // The peer holds the scores' other half of the dims: swap, then add (below).
+            // (Sending the next tile's scores in front of this one's weights instead took
+            // half as long again: it keeps the weights from P.V.)
             if (ok && n_own > 0)
               ok = mbar_wait_cluster(&xfree[wg * 4 + qd], (n_own - 1) & 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);
-            float4 *mine_x = xs + wg * (Cfg::XB / 16) + r;
             if (ok) {
-              const uint32_t dst = peer_smem(smem_u32(mine_x), rank ^ 1);
+              const uint32_t dst = peer_smem(smem_u32(xs + wg * (Cfg::XB / 16) + r), rank ^ 1);
 #pragma unroll 1
               for (int ch = 0; ch < TILE / 16; ++ch) {
                 float s[16];
@@ -687,6 +751,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           row_there |= __shfl_sync(0xffffffffu, row_ok ? 1u : 0u, (lane & ~3) + k) << k;
         }
         if (ok) tc_fence_after();
+        const bool few = nrow <= 8;  // rows of one warp: no line is worth the swap
         const int units = final_rows ? DH / 64 : DH / 32;  // 128-byte lines of a row
 #pragma unroll 1
         for (int u = 0; u < units; ++u) {
@@ -710,6 +775,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(oempty);
           }
+          if (few) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (row_ok) st_global_v8(base + u * 128 + k * 32, v + 8 * k);
+            continue;
+          }
           swap_pieces(v, lane);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -724,6 +795,35 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         }
       } else if (lane == 0) {
         mbar_arrive(oempty);
+      }
+      if (p.cuts == nullptr && g.prefix_len == nullptr && !seg.whole()) {
+        // A piece of a cut unit of few rows: the CTA that leaves the last one joins them
+        // (a kernel behind this one took 5 us of a 20 us decode call).
+        const int32_t first = seg.start + g.unit_cost;
+        const int32_t cf = chunk_of(plan.total, p.workers, first);
+        PartSlots at;
+        cut_parts(plan.total, p.workers, cf, seg.start, g.unit_cost, seg.u.n, at);
+        __threadfence();
+        group_sync(9 + wg);
+        if (t128 == 0) {
+          uint32_t *cnt = p.counters + cf * NH + rank;
+          const uint32_t old = atomic_add_acq_rel_gpu(cnt, 1);
+          const bool last = old + 1 == static_cast<uint32_t>(at.n);
+          if (last) *cnt = 0;
+          last_piece[wg] = last ? 1 : 0;
+        }
+        group_sync(9 + wg);
+        if (last_piece[wg] != 0) {
+#pragma unroll 1
+          for (int32_t row = qd; row < nrow; row += 4) {
+            const int32_t rq = row / g.group, rh = row - rq * g.group;
+            const int64_t to = (static_cast<int64_t>(seg.qb * g.qt_seq + rq) * g.batch + seg.b) * Hq +
+                               seg.x * g.group + rh;
+            join_pieces<Cfg::D>(p.own_o + rank * DH, p.own_lse, at, p.rs, row,
+                                p.out + to * Cfg::D + rank * DH,
+                                p.lse != nullptr && rank == 0 ? p.lse + to : nullptr);
+          }
+        }
       }
     }
     take_back_ref();

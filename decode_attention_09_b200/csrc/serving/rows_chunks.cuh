@@ -16,19 +16,33 @@
 
 namespace gdattn {
 
+// Chunk c of n steps cut for `workers`: [chunk_begin(c), chunk_begin(c + 1)), sizes that
+// differ by at most one (equal ones rounded up leave the last workers without any:
+// 1216 steps over 148 workers used 136 of them).
+// With fewer steps than workers the first workers get one each, so that the pieces of
+// a unit sit in consecutive chunks.
+// (All steps of a call fit 32 bits: the host refuses others.)
+GDATTN_HD int32_t chunk_begin(int32_t steps, int32_t workers, int32_t c) {
+  const int32_t n = imin32(steps, workers);
+  return c < n ? static_cast<int32_t>(static_cast<int64_t>(c) * steps / n) : steps;
+}
+GDATTN_HD int32_t chunk_of(int32_t steps, int32_t workers, int32_t step) {
+  const int32_t n = imin32(steps, workers);
+  return static_cast<int32_t>(((static_cast<int64_t>(step) + 1) * n - 1) / steps);
+}
+
 struct RowsPlan {
-  int64_t total;      // steps
-  int64_t chunk;      // steps per worker
-  int64_t cs, ce;     // this worker's steps
-  int64_t prefix_all; // steps of all prefix units
-  int64_t y_start;    // first step of pair y
+  int32_t total;      // steps
+  int32_t cs, ce;     // this worker's steps
+  int32_t prefix_all; // steps of all prefix units
+  int32_t y_start;    // first step of pair y
   int32_t y;          // the own pair that step max(cs, prefix_all) is in
   int32_t prefix_len; // P
   int32_t least_own;
   int32_t bad;
 };
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+__device__ __forceinline__ int32_t warp_sum32(int32_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -51,9 +65,9 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
   const int32_t pairs = g.batch * g.nqb;
   RowsPlan p;
   bool bad = false;
-  int64_t own = 0;
+  int32_t own = 0;
   for (int32_t y = lane; y < pairs; y += 32) own += pair_steps(g, y, bad);
-  own = warp_sum64(own) * g.n_kv_heads;
+  own = warp_sum32(own) * g.n_kv_heads;
   p.prefix_len = 0;
   p.least_own = 0;
   p.prefix_all = 0;
@@ -71,29 +85,26 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
     }
     p.least_own = least == INT32_MAX ? 0 : least;
     p.prefix_all =
-        static_cast<int64_t>(prefix_steps(g, prefix_unit(g, p.prefix_len, p.least_own))) *
-        g.n_kv_heads * g.npb;
+        prefix_steps(g, prefix_unit(g, p.prefix_len, p.least_own)) * g.n_kv_heads * g.npb;
   }
   p.bad = __any_sync(0xffffffffu, bad);
   p.total = p.prefix_all + own;
-  p.chunk = (p.total + workers - 1) / workers;
-  p.cs = p.chunk * c < p.total ? p.chunk * c : p.total;
-  p.ce = p.cs + p.chunk < p.total ? p.cs + p.chunk : p.total;
+  p.cs = chunk_begin(p.total, workers, c);
+  p.ce = chunk_begin(p.total, workers, c + 1);
   // The own pair whose steps reach past the chunk's start.
   p.y = 0;
   p.y_start = p.prefix_all;
   if (p.cs > p.prefix_all) {
-    int64_t base = p.prefix_all;
+    int32_t base = p.prefix_all;
     p.y = pairs;
     for (int32_t y0 = 0; y0 < pairs; y0 += 32) {
       const int32_t y = y0 + lane;
       bool dummy = false;
-      const int64_t span =
-          y < pairs ? static_cast<int64_t>(pair_steps(g, y, dummy)) * g.n_kv_heads : 0;
-      int64_t incl = span;
+      const int32_t span = y < pairs ? pair_steps(g, y, dummy) * g.n_kv_heads : 0;
+      int32_t incl = span;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       incl += base;
@@ -118,7 +129,7 @@ struct RowSegment {
   int32_t b, qb;   // own: sequence and block; prefix: qb is the prefix block
   int32_t unit;    // index among the prefix units, or among the own units
   int32_t L;       // own: the sequence's length
-  int64_t start;   // the unit's first step
+  int32_t start;   // the unit's first step
   bool prefix;
   bool opens;      // first segment of its chunk
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.n; }
@@ -126,7 +137,7 @@ struct RowSegment {
 
 // Walks the segments of a chunk in order; every warp that needs them runs its own.
 struct RowSegments {
-  int64_t pos, ce, cs, prefix_all, y_start;
+  int32_t pos, ce, cs, prefix_all, y_start;
   int32_t y;
   UnitTiles pu;
 
@@ -146,12 +157,12 @@ struct RowSegments {
         const int32_t steps = prefix_steps(g, pu);
         s.prefix = true;
         s.u = pu;
-        s.unit = static_cast<int32_t>(pos / steps);
+        s.unit = pos / steps;
         s.x = s.unit / g.npb;
         s.qb = s.unit - s.x * g.npb;
         s.b = 0;
         s.L = 0;
-        s.start = static_cast<int64_t>(s.unit) * steps;
+        s.start = s.unit * steps;
       } else {
         for (; y < pairs; ++y) {
           bool dummy = false;
@@ -159,21 +170,21 @@ struct RowSegments {
           s.qb = y - s.b * g.nqb;
           s.L = __ldg(g.seqlens + s.b);
           s.u = own_unit(g, s.L, s.qb, dummy);
-          const int64_t span = static_cast<int64_t>(s.u.n + g.unit_cost) * g.n_kv_heads;
+          const int32_t span = (s.u.n + g.unit_cost) * g.n_kv_heads;
           if (y_start + span > pos) break;
           y_start += span;
         }
         if (y >= pairs) return false;
         s.prefix = false;
-        s.x = static_cast<int32_t>((pos - y_start) / (s.u.n + g.unit_cost));
+        s.x = (pos - y_start) / (s.u.n + g.unit_cost);
         s.unit = y * g.n_kv_heads + s.x;
-        s.start = y_start + static_cast<int64_t>(s.x) * (s.u.n + g.unit_cost);
+        s.start = y_start + s.x * (s.u.n + g.unit_cost);
       }
-      const int64_t first = s.start + g.unit_cost;  // its first tile's step
+      const int32_t first = s.start + g.unit_cost;  // its first tile's step
       s.opens = s.start <= cs;
-      s.t0 = pos > first ? static_cast<int32_t>(pos - first) : 0;
-      s.t1 = ce <= first ? 0 : ce - first < s.u.n ? static_cast<int32_t>(ce - first) : s.u.n;
-      pos = first + s.u.n < ce ? first + s.u.n : ce;
+      s.t0 = imax32(0, pos - first);
+      s.t1 = imin32(ce - first, s.u.n);  // (negative: none)
+      pos = imin32(first + s.u.n, ce);
       if (s.t1 > s.t0) return true;  // (else the chunk ends in front of the first tile)
     }
     return false;
@@ -195,11 +206,11 @@ struct PartSlots {
 };
 
 // Call with a prefix: a unit of its kind whose n > 0 tiles start at step `first`.
-GDATTN_HD PartSlots unit_parts(int64_t chunk, int64_t first, int32_t n, int32_t unit) {
-  const int32_t cf = static_cast<int32_t>(first / chunk);
-  const int32_t cl = static_cast<int32_t>((first + n - 1) / chunk);
+GDATTN_HD PartSlots unit_parts(int32_t steps, int32_t workers, int32_t first, int32_t n,
+                               int32_t unit) {
+  const int32_t cf = chunk_of(steps, workers, first);
   PartSlots s;
-  s.n = cl - cf + 1;
+  s.n = chunk_of(steps, workers, first + n - 1) - cf + 1;
   s.step = 1;
   s.first = partial_slot(true, cf, unit, false);
   s.next = s.first + 1;
@@ -208,13 +219,14 @@ GDATTN_HD PartSlots unit_parts(int64_t chunk, int64_t first, int32_t n, int32_t 
 
 // Call without a prefix: whether the boundary behind chunk c is the first one among
 // the tiles of the unit that starts at step `start` and has n tiles, and its pieces.
-GDATTN_HD bool cut_parts(int64_t chunk, int32_t c, int64_t start, int32_t unit_cost, int32_t n,
-                         PartSlots &s) {
-  const int64_t first = start + unit_cost, here = chunk * (c + 1);
-  if (first >= here || here >= first + n) return false;  // not among its tiles
-  if (first < chunk * c) return false;                   // cut by an earlier boundary
-  s.n = static_cast<int32_t>((first + n - 1) / chunk) - c + 1;
-  s.first = partial_slot(false, c, 0, start <= chunk * c);
+GDATTN_HD bool cut_parts(int32_t steps, int32_t workers, int32_t c, int32_t start,
+                         int32_t unit_cost, int32_t n, PartSlots &s) {
+  const int32_t first = start + unit_cost, here = chunk_begin(steps, workers, c + 1);
+  if (first >= here || here >= first + n) return false;        // not among its tiles
+  const int32_t begin = chunk_begin(steps, workers, c);
+  if (first < begin) return false;                             // cut by an earlier boundary
+  s.n = chunk_of(steps, workers, first + n - 1) - c + 1;
+  s.first = partial_slot(false, c, 0, start <= begin);
   s.next = partial_slot(false, c + 1, 0, true);
   s.step = 2;
   return true;
@@ -228,34 +240,32 @@ struct CutEntry {
   PartSlots parts;
   int32_t b, qb, x, pad;
 };
-// With a prefix, written by worker 0: the chunk, a prefix unit's steps and tiles and the
+// With a prefix, written by worker 0: all steps, a prefix unit's steps and tiles and the
 // first steps of the own pairs.
 struct PrefixEntry {
-  int64_t chunk;
-  int32_t prefix_steps, prefix_tiles;
+  int32_t steps, prefix_steps, prefix_tiles;
 };
 
 // Run by one whole warp, for worker 0 of a call with a prefix.
 __device__ __forceinline__ void write_pair_starts(const RowsGeom &g, const RowsPlan &p,
-                                                  PrefixEntry *entry, int64_t *pair_start) {
+                                                  PrefixEntry *entry, int32_t *pair_start) {
   const int lane = threadIdx.x & 31;
   const int32_t pairs = g.batch * g.nqb;
   if (lane == 0) {
     const UnitTiles pu = prefix_unit(g, p.prefix_len, p.least_own);
-    entry->chunk = p.chunk;
+    entry->steps = p.total;
     entry->prefix_steps = prefix_steps(g, pu);
     entry->prefix_tiles = pu.n;
   }
-  int64_t base = p.prefix_all;
+  int32_t base = p.prefix_all;
   for (int32_t y0 = 0; y0 < pairs; y0 += 32) {
     const int32_t y = y0 + lane;
     bool dummy = false;
-    const int64_t span =
-        y < pairs ? static_cast<int64_t>(pair_steps(g, y, dummy)) * g.n_kv_heads : 0;
-    int64_t incl = span;
+    const int32_t span = y < pairs ? pair_steps(g, y, dummy) * g.n_kv_heads : 0;
+    int32_t incl = span;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
     if (y < pairs) pair_start[y] = base + incl - span;

@@ -187,15 +187,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_prefix_kernel(const RowsP
   grid_launch_dependents();
   grid_dependency_wait();
   const PrefixEntry entry = *p.prefix_entry;
-  const int64_t start = p.pair_start[y];
-  const int32_t steps = static_cast<int32_t>((p.pair_start[y + 1] - start) / g.n_kv_heads);
+  const int32_t start = p.pair_start[y];
+  const int32_t steps = (p.pair_start[y + 1] - start) / g.n_kv_heads;
   if (entry.prefix_tiles > 0) {
     const int32_t unit = x * g.npb + pb;
-    src[0].at = unit_parts(entry.chunk, static_cast<int64_t>(unit) * entry.prefix_steps + g.unit_cost,
+    src[0].at = unit_parts(entry.steps, p.workers,
+                           unit * entry.prefix_steps + g.unit_cost,
                            entry.prefix_tiles, unit);
   }
-  src[1].at = unit_parts(entry.chunk, start + static_cast<int64_t>(x) * steps + g.unit_cost,
-                         steps - g.unit_cost, y * g.n_kv_heads + x);
+  src[1].at = unit_parts(entry.steps, p.workers,
+                         start + x * steps + g.unit_cost, steps - g.unit_cost, y * g.n_kv_heads + x);
   merge_row<D>(src, real, p.merge_shares, p.out + row * D,
                p.lse != nullptr ? p.lse + row : nullptr);
 }

@@ -98,6 +98,11 @@ __device__ __forceinline__ void pair_arrive(int id) {
   asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
 }
 
+// The four warps of a softmax group, on named barrier `id`.
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+
 // The n lowest bits set (none for n <= 0, all for n >= 64).
 __device__ __forceinline__ uint64_t low_bits(int32_t n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;

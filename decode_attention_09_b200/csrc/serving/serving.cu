@@ -107,6 +107,16 @@ int max_workers(const gdattn_layer_desc *d) {
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            nh == 1 ? RowsConfig<1>::SMEM : RowsConfig<2>::SMEM) != cudaSuccess)
     return 0;
+  // The merge runs between row kernels: with the same split of L1 and shared memory the
+  // SMs need no reconfiguration, which each way waits for an idle SM.
+  const void *merges[2] = {nh == 1 ? reinterpret_cast<const void *>(merge_cut_units_kernel<256>)
+                                   : reinterpret_cast<const void *>(merge_cut_units_kernel<512>),
+                           nh == 1 ? reinterpret_cast<const void *>(merge_prefix_kernel<256>)
+                                   : reinterpret_cast<const void *>(merge_prefix_kernel<512>)};
+  for (const void *m : merges)
+    if (cudaFuncSetAttribute(m, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+      return 0;
   int got = 0;
   if (nh == 1) {
     got = sm_count();
@@ -157,13 +167,23 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
   const int64_t own_slots = prefix_rows > 0 ? lay.workers + own_units : 2 * lay.workers;
   const int64_t pre_slots =
       prefix_rows > 0 ? lay.workers + static_cast<int64_t>(g.npb) * g.n_kv_heads : 0;
-  if (own_slots > INT32_MAX || pre_slots > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
+  // Slots, and the steps that the kernels count in 32 bits.
+  const int64_t reach = static_cast<int64_t>(d->window) + g.qt_seq + n_sink;  // of a block
+  const int64_t own_rows_most =
+      d->window > 0 && reach < d->cache_capacity ? reach : d->cache_capacity;
+  const int64_t most_steps =
+      own_units * (own_rows_most / kRowTile + 4 + g.unit_cost) +
+      (prefix_rows > 0 ? static_cast<int64_t>(g.npb) * g.n_kv_heads *
+                             (prefix_rows / kRowTile + 1 + g.unit_cost)
+                       : 0);
+  if (own_slots > INT32_MAX || pre_slots > INT32_MAX || most_steps > INT32_MAX)
+    return GDATTN_ERR_UNSUPPORTED;
   const size_t own_rows = static_cast<size_t>(own_slots) * lay.rs;
   const size_t pre_rows = static_cast<size_t>(pre_slots) * lay.rp;
   // Behind the header: what the row kernel tells the merge.
   lay.table = kHeaderBytes;
   const size_t table_bytes =
-      prefix_rows > 0 ? 256 + (static_cast<size_t>(batch) * g.nqb + 1) * sizeof(int64_t)
+      prefix_rows > 0 ? 256 + (static_cast<size_t>(batch) * g.nqb + 1) * sizeof(int32_t)
                       : static_cast<size_t>(lay.workers) * sizeof(CutEntry);
   lay.own_lse = align256(lay.table + table_bytes);
   lay.pre_lse = align256(lay.own_lse + own_rows * 4);
@@ -232,9 +252,13 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   p.own_lse = reinterpret_cast<float *>(ws + lay.own_lse);
   p.pre_o = reinterpret_cast<float *>(ws + lay.pre_o);
   p.pre_lse = reinterpret_cast<float *>(ws + lay.pre_lse);
-  p.cuts = reinterpret_cast<CutEntry *>(ws + lay.table);
+  // A block of few rows is joined by the row kernel itself; with more rows the four warps
+  // that would do it take longer than a kernel with a warp for each.
+  const bool join_here = prefix_len == nullptr && lay.rs <= 16;
+  p.cuts = join_here ? nullptr : reinterpret_cast<CutEntry *>(ws + lay.table);
+  p.counters = reinterpret_cast<uint32_t *>(ws + kOffCounters);
   p.prefix_entry = reinterpret_cast<PrefixEntry *>(ws + lay.table);
-  p.pair_start = reinterpret_cast<int64_t *>(ws + lay.table + 256);
+  p.pair_start = reinterpret_cast<int32_t *>(ws + lay.table + 256);
   p.status = reinterpret_cast<uint32_t *>(ws);
   p.workers = lay.workers;
   p.rs = lay.rs;
@@ -258,6 +282,7 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = rows_launch(lay.nh, lay.workers, stream, attr);
   if (cudaLaunchKernelEx(&cfg, rows_kernel(desc), m, p) != cudaSuccess) return GDATTN_ERR_CUDA;
+  if (join_here) return GDATTN_OK;
   const cudaError_t e =
       lay.nh == 1 ? launch_merge<256>(lay, p, stream) : launch_merge<512>(lay, p, stream);
   return e == cudaSuccess ? GDATTN_OK : GDATTN_ERR_CUDA;
@@ -434,7 +459,7 @@ gdattn_status gdattn_cache_write_fp8(const void *k_rows, const void *v_rows, int
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   const int64_t ctas = ceil_div(static_cast<int64_t>(n_rows) * desc->n_kv_heads,
-                                kCacheWriteThreads / 32 * kFp8Rows);
+                                kCacheWriteThreads / (desc->head_dim / 32));
   if (ctas > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(ctas), v_rows ? 2 : 1);
   if (desc->head_dim == 256)

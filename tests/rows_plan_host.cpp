@@ -158,7 +158,11 @@ void check_case(std::mt19937_64 &rng, int k) {
     pl = plan_of(g, c, workers);
     if (expect_bad && !pl.bad) fail("impossible lengths went unnoticed", k);
     if (pl.cs != steps_done) fail("chunks do not follow one another", k);
-    if (pl.ce - pl.cs > pl.chunk) fail("chunk too long", k);
+    const int32_t busy = std::min(workers, pl.total);
+    if (pl.ce - pl.cs > pl.total / busy + 1 || (c < busy && pl.ce - pl.cs < pl.total / busy))
+      fail("uneven chunks", k);
+    for (int32_t f = pl.cs; f < pl.ce; ++f)
+      if (chunk_of(pl.total, workers, f) != c) fail("chunk_of", k);
     steps_done = pl.ce;
     RowSegments it;
     it.init(g, pl);
@@ -180,7 +184,7 @@ void check_case(std::mt19937_64 &rng, int k) {
       if (unit_of.count(id) && unit_of[id].start != s.start) fail("a unit's start moves", k);
       unit_of[id] = s;
       if (with_prefix || !s.whole()) {
-        const int64_t slot = partial_slot(with_prefix, c, s.unit, s.opens);
+        const int32_t slot = partial_slot(with_prefix, c, s.unit, s.opens);
         const int64_t units = s.prefix ? static_cast<int64_t>(g.npb) * g.n_kv_heads
                                        : static_cast<int64_t>(g.batch) * g.nqb * g.n_kv_heads;
         if (slot < 0 || slot >= (with_prefix ? workers + units : 2 * workers))
@@ -224,14 +228,14 @@ void check_case(std::mt19937_64 &rng, int k) {
   };
   if (with_prefix) {
     for (const auto &e : pieces)
-      expect_parts(e.first, unit_parts(pl.chunk, unit_of[e.first].start + g.unit_cost,
+      expect_parts(e.first, unit_parts(pl.total, workers, unit_of[e.first].start + g.unit_cost,
                                        unit_of[e.first].u.n, e.first.second));
   } else {
     for (int32_t c = 0; c + 1 < workers; ++c) {
       if (!has_first[c + 1]) continue;
       const RowSegment &s = first_of[c + 1];
       PartSlots ps;
-      if (cut_parts(pl.chunk, c, s.start, g.unit_cost, s.u.n, ps)) {
+      if (cut_parts(pl.total, workers, c, s.start, g.unit_cost, s.u.n, ps)) {
         const std::pair<bool, int32_t> id(false, s.unit);
         if (merged.count(id)) fail("a unit is merged twice", k);
         expect_parts(id, ps);

@@ -58,9 +58,11 @@ def test_row_planner(tmp_path):
     ("if (imax32(lo, g.sinks) < oldest) {", "if (lo < oldest - 2 * g.capacity - 100000) {"),
     ("return prefix_call ? c + unit : 2 * c + (opens ? 0 : 1);",
      "return prefix_call ? c + unit : 2 * c;"),
-    ("if (first < chunk * c) return false;", "if (first < 0) return false;"),
-    ("s.first = partial_slot(false, c, 0, start <= chunk * c);",
-     "s.first = partial_slot(false, c, 0, first <= chunk * c);"),
+    ("if (first < begin) return false; ", "if (first < 0) return false; "),
+    ("s.first = partial_slot(false, c, 0, start <= begin);",
+     "s.first = partial_slot(false, c, 0, first <= begin);"),
+    ("return static_cast<int32_t>(((static_cast<int64_t>(step) + 1) * n - 1) / steps);",
+     "return static_cast<int32_t>(static_cast<int64_t>(step) * n / steps);"),
     ("s.opens = s.start <= cs;", "s.opens = s.start < cs;"),
     ("if (y_start + span > pos) break;", "if (y_start + span >= pos) break;"),
 ])

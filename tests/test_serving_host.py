@@ -200,7 +200,7 @@ def test_query_tensors(any_device):
     with pytest.raises(ValueError, match="out: .* the call reaches"):
         binding._check_tokens(q, cache, cache, lens, q[:1], lse, d)
     with pytest.raises(ValueError, match="workspace: dtype"):
-        binding._check_workspace(lse, None)
+        binding._check_workspace(lse, q, q.get_device())
 
 
 # ------------------------------------------------------------ definitions
