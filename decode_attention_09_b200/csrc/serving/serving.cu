@@ -138,10 +138,6 @@ struct RowsLayout {
 // Blocks, workers and workspace of a call (prefix_rows 0: a call without a prefix).
 gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_desc *d,
                           int32_t n_sink, int32_t prefix_rows, RowsLayout &lay) {
-  const int most = max_workers(d);
-  if (most <= 0) return GDATTN_ERR_CUDA;
-  lay.nh = d->head_dim / 256;
-  lay.workers = d->split_ctas > 0 && d->split_ctas < most ? d->split_ctas : most;
   RowsGeom &g = lay.g;
   g.batch = batch;
   g.tokens = n_tokens;
@@ -164,10 +160,7 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
   g.unit_cost = lay.rs > 32 ? 3 : 1;
   lay.rp = g.qt_pre * g.group;
   const int64_t own_units = static_cast<int64_t>(batch) * g.nqb * g.n_kv_heads;
-  const int64_t own_slots = prefix_rows > 0 ? lay.workers + own_units : 2 * lay.workers;
-  const int64_t pre_slots =
-      prefix_rows > 0 ? lay.workers + static_cast<int64_t>(g.npb) * g.n_kv_heads : 0;
-  // Slots, and the steps that the kernels count in 32 bits.
+  // The kernels count steps in 32 bits.
   const int64_t reach = static_cast<int64_t>(d->window) + g.qt_seq + n_sink;  // of a block
   const int64_t own_rows_most =
       d->window > 0 && reach < d->cache_capacity ? reach : d->cache_capacity;
@@ -176,8 +169,15 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
       (prefix_rows > 0 ? static_cast<int64_t>(g.npb) * g.n_kv_heads *
                              (prefix_rows / kRowTile + 1 + g.unit_cost)
                        : 0);
-  if (own_slots > INT32_MAX || pre_slots > INT32_MAX || most_steps > INT32_MAX)
-    return GDATTN_ERR_UNSUPPORTED;
+  if (most_steps > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
+  const int most = max_workers(d);
+  if (most <= 0) return GDATTN_ERR_CUDA;
+  lay.nh = d->head_dim / 256;
+  lay.workers = d->split_ctas > 0 && d->split_ctas < most ? d->split_ctas : most;
+  const int64_t own_slots = prefix_rows > 0 ? lay.workers + own_units : 2 * lay.workers;
+  const int64_t pre_slots =
+      prefix_rows > 0 ? lay.workers + static_cast<int64_t>(g.npb) * g.n_kv_heads : 0;
+  if (own_slots > INT32_MAX || pre_slots > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
   const size_t own_rows = static_cast<size_t>(own_slots) * lay.rs;
   const size_t pre_rows = static_cast<size_t>(pre_slots) * lay.rp;
   // Behind the header: what the row kernel tells the merge.

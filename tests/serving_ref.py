@@ -39,8 +39,11 @@ class Case:
 
 
 def make_case(seed, T, lens, hq, hkv, dim, window, sinks=0, capacity=None, shared=False,
-              softcap=0.0, prefix=None, prefix_rows=None, heavy=1.0, device="cpu") -> Case:
-    """lens: own tokens per sequence.  The ring holds what the T tokens' windows reach."""
+              softcap=0.0, prefix=None, prefix_rows=None, heavy=1.0, growth=0.0, scale=None,
+              q_scale=1.0) -> Case:
+    """lens: own tokens per sequence.  The ring holds what the T tokens' windows reach.
+    heavy multiplies the pinned rows of K, and growth makes K rows grow with their
+    position (to 1 + growth times as large), so that a row's maximum keeps moving."""
     g = torch.Generator().manual_seed(seed)
 
     def normal(*shape):
@@ -58,6 +61,8 @@ def make_case(seed, T, lens, hq, hkv, dim, window, sinks=0, capacity=None, share
     for b, L in enumerate(lens):
         kr = normal(max(L, 0), hkv, dim)
         kr[:sinks] *= heavy
+        if growth:
+            kr *= (1 + growth * torch.arange(len(kr)) / max(1, len(kr)))[:, None, None].to(kr.dtype)
         vr = kr if shared else normal(max(L, 0), hkv, dim)
         pos = torch.arange(max(L, 0))
         low = max(0, L - T + 1 - window) if window else 0  # first window's start
@@ -68,8 +73,9 @@ def make_case(seed, T, lens, hq, hkv, dim, window, sinks=0, capacity=None, share
             v[b, at] = vr[pos]
         k_rows.append(kr)
         v_rows.append(vr)
-    c = Case(normal(T, B, hq, dim), k_rows, v_rows, k, v, torch.tensor(lens, dtype=torch.int32),
-             window, sinks, capacity, softcap, 1.0 / math.sqrt(dim))
+    c = Case(normal(T, B, hq, dim) * q_scale, k_rows, v_rows, k, v, torch.tensor(lens, dtype=torch.int32),
+             window, sinks, capacity, softcap,
+             1.0 / math.sqrt(dim) if scale is None else scale)
     if prefix is not None:
         rows = prefix_rows or max(1, prefix)
         c.pk = torch.full((rows, hkv, dim), NAN, dtype=torch.bfloat16)
@@ -125,7 +131,7 @@ def reference(c: Case, device="cpu") -> Ref:
         for h in range(Hq):
             kh, vh = k[:, h // G], v[:, h // G]
             x = q[:, h] @ kh.T * c.scale
-            mag = (q[:, h].abs() @ kh.abs().T * c.scale).masked_fill(~see, 0.0).amax(-1)
+            mag = (q[:, h].abs() @ kh.abs().T * abs(c.scale)).masked_fill(~see, 0.0).amax(-1)
             if c.softcap:
                 x = c.softcap * torch.tanh(x / c.softcap)
             x = x.masked_fill(~see, -math.inf)

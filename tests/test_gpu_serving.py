@@ -92,6 +92,20 @@ SINKS = {
     "group16_shared": dict(T=9, lens=[150, 40], window=70, sinks=4, hq=16, hkv=1, dim=256,
                            shared=True),
     "group128": dict(T=2, lens=[90], window=70, sinks=4, hq=128, hkv=1, dim=256),
+    "growing_scores": dict(T=3, lens=[900, 400], window=700, sinks=4, growth=15.0, **SLIDING),
+    "growing_scores_chunk": dict(T=100, lens=[400], window=300, sinks=4, growth=20.0, **SLIDING),
+    "large_scores": dict(T=1, lens=[300, 70], window=200, sinks=4, q_scale=64.0, **SLIDING),
+    "capped_large_scores": dict(T=1, lens=[300, 70], window=200, sinks=4, q_scale=64.0,
+                                softcap=20.0, **SLIDING),
+    "scale_zero": dict(T=2, lens=[150, 64], window=100, sinks=4, scale=0.0, **SLIDING),
+    "scale_negative": dict(T=2, lens=[150, 64], window=100, sinks=4, scale=-0.05, **SLIDING),
+    "scale_negative_capped": dict(T=2, lens=[150, 64], window=100, sinks=4, scale=-0.05,
+                                  softcap=5.0, **SLIDING),
+    "many_sequences": dict(T=1, lens=[(7 * i) % 90 for i in range(333)], window=40, sinks=3, hq=2,
+                           hkv=1, dim=256),
+    "group100": dict(T=3, lens=[90, 3], window=70, sinks=4, hq=100, hkv=1, dim=256),
+    "wide_growing": dict(T=20, lens=[400], window=300, sinks=4, growth=20.0, hq=16, hkv=1,
+                         dim=512, shared=True),
     "wide_shared": dict(T=1, lens=[300, 20, 0], window=100, sinks=4, hq=16, hkv=1, dim=512,
                         shared=True),
     "wide_shared_chunk": dict(T=40, lens=[300, 41], window=100, sinks=4, hq=16, hkv=1, dim=512,
@@ -131,6 +145,9 @@ PREFIX = {
                             **SLIDING),
     "group4": dict(T=2, lens=[40, 3], prefix=100, hq=8, hkv=2, dim=256, window=0),
     "group3": dict(T=1, lens=[40, 3, 8], prefix=100, hq=9, hkv=3, dim=256, window=50),
+    "scale_negative": dict(T=1, lens=[40, 3, 8], prefix=100, scale=-0.1, **GLOBAL),
+    "growing": dict(T=2, lens=[300, 40], prefix=400, growth=20.0, **GLOBAL),
+    "group128": dict(T=1, lens=[40, 3], prefix=100, hq=128, hkv=1, dim=512, window=0),
     "group16_shared": dict(T=1, lens=[40, 3], prefix=100, hq=16, hkv=1, dim=256, shared=True,
                            window=0),
 }
@@ -284,3 +301,247 @@ def test_fp8_codes_of_every_pair_of_mantissas():
     value, s = ref.e4m3_rows(rows)
     assert torch.equal(scale.cpu().view(-1).double(), s)
     assert torch.equal(codes.cpu().view(n, D).view(torch.float8_e4m3fn).double(), value)
+
+
+# --------------------------------------------------- errors seen by the device
+@pytest.mark.parametrize("dim,hkv,shared", [(256, 8, False), (512, 1, True)])
+@pytest.mark.parametrize("split", [0, 5])
+def test_sequences_shorter_than_the_step(dim, hkv, shared, split):
+    """0 < L < T is reported; the tokens that have a position are right, the others 0."""
+    c = ref.make_case(1, 9, [4, 30, 0, 8], 16, hkv, dim, window=20, sinks=3, shared=shared)
+    run_and_check(c, split, status=binding.GDATTN_ERR_DEVICE_SEQLEN)
+
+
+def test_negative_and_too_long_lengths_are_reported():
+    c = ref.make_case(2, 1, [40, 40, 40], 16, 8, 256, window=20, sinks=3, capacity=23)
+    good = Call(c, max_seqlen=1000).run()[0].clone()
+    call = Call(c, max_seqlen=1000)
+    call.args[3] = torch.tensor([40, -7, 40], dtype=torch.int32, device="cuda")
+    out, lse = call.run(binding.GDATTN_ERR_DEVICE_SEQLEN)
+    assert torch.equal(out[:, [0, 2]], good[:, [0, 2]])
+    assert (out[:, 1] == 0).all() and (lse[:, 1] == -float("inf")).all()
+    # Longer than the ring can serve: never outside the cache, the others untouched.
+    c = ref.make_case(3, 1, [40, 64], 16, 1, 512, window=0, prefix=30, shared=True)
+    good = Call(c).run()[0].clone()
+    call = Call(c)
+    call.args[3] = torch.tensor([40, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    out, _ = call.run(binding.GDATTN_ERR_DEVICE_SEQLEN)
+    assert torch.equal(out[:, 0], good[:, 0])
+
+
+@pytest.mark.parametrize("plen", [-5, 65])
+def test_prefix_length_out_of_range_is_clamped(plen):
+    c = ref.make_case(4, 1, [9, 70], 16, 1, 512, window=0, prefix=64 if plen > 0 else 0,
+                      prefix_rows=64, shared=True)
+    call = Call(c)
+    call.prefix[2].fill_(plen)
+    out, lse = call.run(binding.GDATTN_ERR_DEVICE_SEQLEN)
+    ref.check(out, lse, ref.reference(c, "cuda"))
+
+
+@pytest.mark.parametrize("kind", ["sink", "prefix", "wide"])
+def test_a_wait_that_runs_out_is_reported(kind):
+    """Every CTA leaves its first K tile unloaded: the call ends, says so, and a
+    re-initialised workspace then gives the right result."""
+    args = dict(sink=dict(T=1, lens=[500, 90], window=300, sinks=4, **SLIDING),
+                prefix=dict(T=1, lens=[9, 30], prefix=200, **GLOBAL),
+                wide=dict(T=2, lens=[300, 20], window=100, sinks=4, hq=16, hkv=2, dim=512))[kind]
+    c = ref.make_case(5, **args)
+    call = Call(c, flags=binding.GDATTN_FLAG_TEST_WITHHOLD_KV)
+    call.run(binding.GDATTN_ERR_DEVICE_TIMEOUT)
+    call.desc.flags = 0
+    binding.workspace_init(call.ws.t)
+    out, lse = call.run()
+    ref.check(out, lse, ref.reference(c, "cuda"))
+
+
+# ----------------------------------------------- streams, graphs, workspaces
+def test_captured_call_follows_lengths_and_prefix():
+    """One graph, replayed with other lengths, another prefix length and other rows."""
+    for kind in ("sink", "prefix"):
+        base = dict(T=2, window=100, sinks=4, **SLIDING) if kind == "sink" else dict(T=1, **GLOBAL)
+        more = {} if kind == "sink" else dict(prefix_rows=200)
+        cases = []
+        for k, lens in enumerate(([150, 30, 0], [2, 99, 260], [101, 102, 3])):
+            cap = 105 if kind == "sink" else 260
+            px = {} if kind == "sink" else dict(prefix=(200, 77, 0)[k])
+            cases.append(ref.make_case(k, lens=lens, capacity=cap, **base, **more, **px))
+        call = Call(cases[0], max_seqlen=1000)
+        call.run()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call.enqueue()
+        for c in cases + cases[::-1]:
+            for t, new in zip(call.args, (c.q, c.k, c.v, c.lens)):
+                if t is not None:
+                    t.copy_(new)
+            if call.prefix:
+                call.prefix[0].copy_(c.pk)
+                call.prefix[2].fill_(c.plen)
+            graph.replay()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert binding.check_device_status(call.ws.t) == binding.GDATTN_OK
+            ref.check(call.out.t, call.lse.t, ref.reference(c, "cuda"), kind)
+
+
+def test_calls_on_two_streams_with_their_own_workspaces():
+    cases = [ref.make_case(k, T=1, lens=[900 + k, 70], window=500, sinks=4, **SLIDING)
+             for k in range(2)]
+    calls = [Call(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        for call, s in zip(calls, streams):
+            call.enqueue(stream=s)
+    torch.cuda.synchronize()
+    for call, c in zip(calls, cases):
+        assert binding.check_device_status(call.ws.t) == binding.GDATTN_OK
+        ref.check(call.out.t, call.lse.t, ref.reference(c, "cuda"))
+
+
+def test_one_workspace_serves_different_calls_in_turn():
+    """Sinks, prefix and the decode kernels that were there, back to back on one
+    workspace, each call's result as alone and bit for bit the same every time."""
+    cases = [ref.make_case(1, T=1, lens=[900, 70, 300], window=500, sinks=4, **SLIDING),
+             ref.make_case(2, T=1, lens=[9, 300], prefix=333, **GLOBAL),
+             ref.make_case(3, T=70, lens=[90, 71], window=60, sinks=4, **SLIDING),
+             ref.make_case(4, T=1, lens=[700, 2], window=0, prefix=100, **SLIDING)]
+    calls = [Call(c) for c in cases]
+    d = binding.make_desc(16, 8, 256, 500, 0.0, 1 / 16, False, 512)
+    q = torch.randn((3, 16, 256), device="cuda").to(torch.bfloat16)
+    kv = torch.randn((2, 3, 512, 8, 256), device="cuda").to(torch.bfloat16)
+    lens = torch.tensor([900, 70, 300], dtype=torch.int32, device="cuda")
+    n = max([binding.workspace_size(3, 900, d)] + [call.ws.t.numel() for call in calls])
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    binding.workspace_init(ws)
+    want = [tuple(t.clone() for t in call.run()) for call in calls]
+    old = binding.decode(q, kv[0], kv[1], lens, d, 900)
+    for call in calls:
+        call.ws.t = ws
+    for _ in range(5):
+        for call in calls:
+            call.out.t.fill_(float("nan"))
+            call.enqueue()
+            got = binding.decode(q, kv[0], kv[1], lens, d, 900, workspace=ws)
+            assert torch.equal(got[0], old[0]) and torch.equal(got[1], old[1])
+        for call, w in zip(calls, want):
+            assert torch.equal(call.out.t, w[0]) and torch.equal(call.lse.t, w[1])
+    assert binding.check_device_status(ws) == binding.GDATTN_OK
+
+
+def test_strided_caches_and_offsets_past_32_bits():
+    """Sequences far apart in one buffer: more than 2^31 elements in front of the last."""
+    c = ref.make_case(6, T=2, lens=[150, 90], window=100, sinks=4, **SLIDING)
+    rows = c.k[0].numel()
+    stride = 2 ** 31 // rows * rows + 8 * rows
+    call = Call(c)
+    big = []
+    for t in (c.k, c.v):
+        flat = torch.empty(stride + rows, dtype=torch.bfloat16, device="cuda")
+        for b in range(2):
+            flat[b * stride:b * stride + rows].copy_(t[b].reshape(-1))
+        big.append(flat.as_strided(c.k.shape, (stride, *c.k[0].stride())))
+    call.args[1:3] = big
+    call.desc.cache_batch_stride = stride
+    out, lse = call.run()
+    ref.check(out, lse, ref.reference(c, "cuda"))
+    # and writes there
+    new = torch.randn((2, 8, 256), device="cuda").to(torch.bfloat16)
+    at = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    slot = torch.tensor([5, 101], dtype=torch.int32, device="cuda")
+    binding.cache_write(new, new, at, slot, call.desc, big[0], big[1])
+    for t in big:
+        assert torch.equal(t[0, 5], new[0]) and torch.equal(t[1, 101], new[1])
+        assert torch.equal(t[1, 80], dev(c.k[1, 80]) if t is big[0] else dev(c.v[1, 80]))
+
+
+def test_a_long_ring_of_many_tiles():
+    """A context far longer than its ring, and a ring of many tiles and pieces."""
+    run_and_check(ref.make_case(7, T=1, lens=[100000], window=5000, sinks=4, hq=2, hkv=1,
+                                dim=256))
+
+
+# -------------------------------------------------------------- as one server
+def test_serving_steps_end_to_end():
+    """Prompts written by a slot map and attended in one chunk, then decode steps of the
+    batch with one token each, sliding layer with pins: every step's output against the
+    definition over all rows so far.  A second layer keeps an fp8 copy of its rows."""
+    g = torch.Generator().manual_seed(0)
+    hq, hkv, dim, window, sinks = 16, 8, 256, 48, 4
+    capacity = sinks + window + 40 - 1
+    B, prompt = 3, [40, 17, 33]
+    desc = binding.make_desc(hq, hkv, dim, window, 30.0, 1 / 16, False, capacity)
+    k = torch.full((B, capacity, hkv, dim), ref.NAN, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    codes = torch.zeros((2, B, capacity, hkv, dim), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((2, B, hkv, capacity), device="cuda")
+    rows = [[torch.zeros((0, hkv, dim), dtype=torch.bfloat16) for _ in range(B)] for _ in range(2)]
+
+    def write(new):
+        n = sum(new)
+        fused = torch.randn((n, hq + 2 * hkv, dim), generator=g).to(torch.bfloat16)
+        at = 0
+        for b, m in enumerate(new):
+            for i in range(2):
+                part = fused[at:at + m, hq + i * hkv:hq + (i + 1) * hkv]
+                rows[i][b] = torch.cat([rows[i][b], part])
+            at += m
+        lens = torch.tensor([len(r) for r in rows[0]], dtype=torch.int32, device="cuda")
+        m = binding.slot_map(lens, torch.tensor(new, dtype=torch.int32, device="cuda"), n + 2,
+                             capacity, sinks)
+        f = torch.cat([fused, fused[:2]]).cuda()  # two rows behind the step's last
+        kr, vr = f[:, hq:hq + hkv], f[:, hq + hkv:]
+        binding.cache_write(kr, vr, m.seq, m.slot, desc, k, v)
+        binding.cache_write_fp8(kr, vr, m.seq, m.slot, desc, codes[0], codes[1], scale[0],
+                                scale[1])
+        return lens
+
+    def attend(T, lens):
+        q = torch.randn((T, B, hq, dim), generator=g).to(torch.bfloat16)
+        out, lse = binding.decode_sink(q.cuda(), k, v, lens, desc, 1000, sinks)
+        c = ref.Case(q, rows[0], rows[1], k.cpu(), v.cpu(), lens.cpu(), window, sinks, capacity,
+                     30.0, 1 / 16)
+        ref.check(out, lse, ref.reference(c, "cuda"), f"T = {T}")
+
+    lens = write(prompt)
+    attend(17, lens)
+    for step in range(60):
+        lens = write([1, 1 if step % 3 else 0, 1])
+        attend(1, lens)
+    # the fp8 copy holds the same rows, rounded
+    slot = ref.slot_of(torch.arange(len(rows[0][0])), sinks, capacity)
+    last = len(rows[0][0]) - 1
+    value, s = ref.e4m3_rows(rows[1][0][last])
+    got = codes[1, 0, slot[last]].cpu().view(torch.float8_e4m3fn).double()
+    assert torch.equal(got, value)
+    assert torch.equal(scale[1, 0, :, slot[last]].cpu().double(), s)
+
+
+def test_fp8_rows_written_here_are_what_the_fp8_decode_reads():
+    """A ring filled by gdattn_cache_write_fp8 and read by gdattn_decode_fp8."""
+    import oracle
+    orc = oracle.get()
+    g = torch.Generator().manual_seed(3)
+    hq, hkv, dim, window = 16, 8, 256, 64
+    lens = [100, 64, 7]
+    B = len(lens)
+    desc = binding.make_desc(hq, hkv, dim, window, 0.0, 1 / 16, False, window)
+    codes = torch.zeros((2, B, window, hkv, dim), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((2, B, hkv, window), device="cuda")
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    m = binding.slot_map(lens_t, lens_t, sum(lens), window)
+    kv = [torch.randn((sum(lens), hkv, dim), generator=g).to(torch.bfloat16).cuda()
+          for _ in range(2)]
+    binding.cache_write_fp8(kv[0], kv[1], m.seq, m.slot, desc, codes[0], codes[1], scale[0],
+                            scale[1])
+    q = torch.randn((B, hq, dim), generator=g).to(torch.bfloat16)
+    out, lse = binding.decode_fp8(q.cuda(), codes[0], codes[1], scale[0], scale[1], lens_t, desc,
+                                  max(lens))
+    o_ref, l_ref = orc.decode_fp8(q, codes[0].cpu(), codes[1].cpu(), scale[0].cpu(),
+                                  scale[1].cpu(), lens_t.cpu(), window, 0.0, 1 / 16)
+    # the entry point's own gates
+    assert (out.cpu().double() - torch.as_tensor(o_ref)).abs().max() <= 8e-3
+    assert (lse.cpu().double() - torch.as_tensor(l_ref)).abs().max() <= 1e-3

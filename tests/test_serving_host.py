@@ -98,6 +98,14 @@ def test_prefix_refusals(kw, expect):
     assert prefix(**kw) == expect
 
 
+def test_more_work_than_32_bits_count_is_refused():
+    """2^20 tokens of one sequence, each over up to 2^20 positions."""
+    d = shared(cache_capacity=1 << 20)
+    assert prefix(d, T=1 << 20, max_seqlen=1 << 20) == UNSUPPORTED
+    many = shared(n_q_heads=128, cache_capacity=64)  # batch * T * Hq above 2^31 - 1
+    assert prefix(many, batch=1 << 20, T=17) == UNSUPPORTED
+
+
 def test_workspace_queries_refuse():
     assert binding.sink_workspace_size(0, 1, 8, sliding(), 4) == 0
     assert binding.sink_workspace_size(1, 1, 8192, sliding(window=0), 4) == 0
