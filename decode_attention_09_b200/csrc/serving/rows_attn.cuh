@@ -62,6 +62,7 @@ struct RowsConfig {
   static constexpr int D = DH * NH;
   static constexpr int M = 128;                     // query rows per block
   static constexpr int TILE = kRowTile;
+  static constexpr int CW = 16;                     // score columns a softmax loop takes at once
   static constexpr int BOXB = TILE * 128;           // 64 rows x 64 dims: 8 KiB
   static constexpr int TB = BOXB * (DH / 64);       // a tile: 32 KiB
   static constexpr int NST = NH == 1 ? 5 : 3;       // ring
@@ -130,7 +131,7 @@ __device__ __forceinline__ uint32_t v_entry(uint32_t i) {
 // Joins the pieces of one row of a cut unit, 256 dims of it, by one warp:
 //   lse = log2 sum_i 2^lse_i,  out = sum_i 2^(lse_i - lse) o_i.
 template <int D>
-__device__ __noinline__ void join_pieces(const float *o, const float *lse, const PartSlots &at,
+__device__ __forceinline__ void join_pieces(const float *o, const float *lse, const PartSlots &at,
                                             int32_t rows, int32_t r, uint16_t *out,
                                             float *out_lse) {
   constexpr int kFlight = 4;
@@ -184,7 +185,7 @@ template <int NH, bool SHARED, bool CAP>
 __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     rows_attn_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
   using Cfg = RowsConfig<NH>;
-  constexpr int DH = Cfg::DH, NST = Cfg::NST, TILE = Cfg::TILE;
+  constexpr int DH = Cfg::DH, NST = Cfg::NST, TILE = Cfg::TILE, CW = Cfg::CW;
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   const uint32_t tmem = *tmem_base_smem;
   const RowsPlan &plan = *plan_smem;
   RowSegments segs;
-  segs.init(g, plan);
+  segs.init(plan);
   RowSegment seg;
 
   if (warp == 0) {
@@ -502,17 +503,13 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       const int32_t tq = r / g.group, h = r - tq * g.group;
       const bool row_ok = r < nrow;
       RowRange rg = {0, 0, 0};
-      int32_t tok = 0, b = 0;
       if (row_ok) {
         const int32_t a = seg.qb * qt + tq;
         if (seg.prefix) {
-          tok = a / g.batch;
-          b = a - tok * g.batch;
-          rg = prefix_row_range(g, __ldg(g.seqlens + b), tok, plan.prefix_len);
+          const int32_t tok = a / g.batch;
+          rg = prefix_row_range(g, __ldg(g.seqlens + a - tok * g.batch), tok, plan.prefix_len);
         } else {
-          tok = a;
-          b = seg.b;
-          rg = own_row_range(g, seg.L, tok);
+          rg = own_row_range(g, seg.L, a);
         }
       }
       const bool act = 32 * qd < nrow;  // the warp has rows (warp-uniform)
@@ -528,7 +525,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         const RowTile tile = unit_tile(seg.u, t);
         const uint32_t s_col = tmem + lane_base + Cfg::S_COL + sb * TILE;
         if (act) {
-          // The tile is walked by 16 columns in loops that stay rolled: the unrolled
+          // The tile is walked by CW columns in loops that stay rolled: the unrolled
           // softmax of 64 columns does not fit the instruction cache beside the other
           // warps' code, and its misses cost more than the second read of the scores
           // from tensor memory.
@@ -543,12 +540,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             if (ok) {
               const uint32_t dst = peer_smem(smem_u32(xs + wg * (Cfg::XB / 16) + r), rank ^ 1);
 #pragma unroll 1
-              for (int ch = 0; ch < TILE / 16; ++ch) {
-                float s[16];
-                tmem_ld16(s_col + 16 * ch, s);
+              for (int ch = 0; ch < TILE / CW; ++ch) {
+                float s[CW];
+                tmem_load(s_col + CW * ch, s);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  st_peer_v4(dst + (4 * ch + c) * (Cfg::M * 16), s[4 * c], s[4 * c + 1],
+                for (int c = 0; c < CW / 4; ++c)
+                  st_peer_v4(dst + (CW / 4 * ch + c) * (Cfg::M * 16), s[4 * c], s[4 * c + 1],
                              s[4 * c + 2], s[4 * c + 3]);
               }
               __syncwarp();
@@ -571,30 +568,30 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // The largest product (times the scale's sign: scale and soft-cap are monotonic).
           float best = -INFINITY;
 #pragma unroll 1
-          for (int ch = 0; ch < TILE / 16; ++ch) {
-            float s[16];
-            if (ok) tmem_ld16(s_col + 16 * ch, s);
+          for (int ch = 0; ch < TILE / CW; ++ch) {
+            float s[CW];
+            if (ok) tmem_load(s_col + CW * ch, s);
             if (NH == 2 && ok) {
-              const float4 *x = xs + wg * (Cfg::XB / 16) + ch * 4 * Cfg::M + r;
+              const float4 *x = xs + wg * (Cfg::XB / 16) + ch * (CW / 4) * Cfg::M + r;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
+              for (int c = 0; c < CW / 4; ++c) {
                 const float4 o = x[c * Cfg::M];
                 s[4 * c] += o.x;
                 s[4 * c + 1] += o.y;
                 s[4 * c + 2] += o.z;
                 s[4 * c + 3] += o.w;
               }
-              tmem_store16(s_col + 16 * ch, s);
+              tmem_store(s_col + CW * ch, s);
             }
-            const uint32_t bits = static_cast<uint32_t>(seen >> (16 * ch));
+            const uint32_t bits = static_cast<uint32_t>(seen >> (CW * ch));
             float m4[4] = {best, best, best, best};
             if (masked) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
+              for (int c = 0; c < CW; ++c)
                 m4[c & 3] = fmaxf(m4[c & 3], (bits >> c) & 1 ? s[c] * sign : -INFINITY);
             } else {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
+              for (int c = 0; c < CW; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
             }
             best = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
@@ -650,30 +647,31 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           const float mr = now == -INFINITY ? 0.f : now;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int ch = 0; ch < TILE / 16; ++ch) {
-            float s[16], w[16];
-            if (ok) tmem_ld16(s_col + 16 * ch, s);
+          for (int ch = 0; ch < TILE / CW; ++ch) {
+            float s[CW], w[CW];
+            if (ok) tmem_load(s_col + CW * ch, s);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < CW; ++c)
               s[c] = CAP ? ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr)
                          : ex2_approx(fmaf(s[c], p.qscale, -mr));
             if (masked) {
-              const uint32_t bits = static_cast<uint32_t>(seen >> (16 * ch));
+              const uint32_t bits = static_cast<uint32_t>(seen >> (CW * ch));
 #pragma unroll
-              for (int c = 0; c < 16; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
+              for (int c = 0; c < CW; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < CW / 2; ++j) {
               const float pa = s[2 * j], pb = s[2 * j + 1];
               l4[j & 3] += pa + pb;
               const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
               const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
               const float rb = pb - __uint_as_float(ub & 0xFFFF0000u);
-              w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
-              w[8 + j] =
+              const int at = j / 8 * 16 + j % 8;  // 8 columns of weights, 8 of remainders
+              w[at] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
+              w[at + 8] =
                   __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
             }
-            if (ok) tmem_store16(s_col + 16 * ch, w);
+            if (ok) tmem_store(s_col + CW * ch, w);
           }
           if (ok) tmem_store_wait();
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
@@ -729,8 +727,9 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       if (act) {
         const float inv = (ok && l > 0.f) ? __fdividef(1.f, l) : 0.f;
         const bool final_rows = g.prefix_len == nullptr && seg.whole();
+        // (the row's token and sequence: only own units write final rows)
         const int64_t orow =
-            (static_cast<int64_t>(tok) * g.batch + b) * Hq + seg.x * g.group + h;
+            (static_cast<int64_t>(seg.qb * qt + tq) * g.batch + seg.b) * Hq + seg.x * g.group + h;
         const int64_t prow =
             static_cast<int64_t>(
                 partial_slot(g.prefix_len != nullptr, worker, seg.unit, seg.opens)) *
@@ -760,10 +759,14 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 32; ++q) v[q] = 0;
           } else if (final_rows) {
-            float o[64];
-            tmem_ld64(tmem + lane_base + Cfg::O_COL + u * 64, o);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = pack_bf16x2(o[2 * q] * inv, o[2 * q + 1] * inv);
+            for (int half = 0; half < 2; ++half) {
+              float o[32];
+              tmem_load32(tmem + lane_base + Cfg::O_COL + u * 64 + half * 32, o);
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                v[16 * half + q] = pack_bf16x2(o[2 * q] * inv, o[2 * q + 1] * inv);
+            }
           } else {
             float o[32];
             tmem_load32(tmem + lane_base + Cfg::O_COL + u * 32, o);

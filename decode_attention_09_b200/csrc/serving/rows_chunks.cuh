@@ -40,6 +40,7 @@ struct RowsPlan {
   int32_t prefix_len; // P
   int32_t least_own;
   int32_t bad;
+  UnitTiles pu;       // of every prefix unit
 };
 
 __device__ __forceinline__ int32_t warp_sum32(int32_t v) {
@@ -70,7 +71,6 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
   own = warp_sum32(own) * g.n_kv_heads;
   p.prefix_len = 0;
   p.least_own = 0;
-  p.prefix_all = 0;
   if (g.prefix_len != nullptr) {
     p.prefix_len = clamp_prefix(g, __ldg(g.prefix_len), bad);
     int32_t least = INT32_MAX;
@@ -84,9 +84,9 @@ __device__ __forceinline__ RowsPlan plan_rows(const RowsGeom &g, int32_t c, int3
         least = imin32(least, __shfl_xor_sync(0xffffffffu, least, o));
     }
     p.least_own = least == INT32_MAX ? 0 : least;
-    p.prefix_all =
-        prefix_steps(g, prefix_unit(g, p.prefix_len, p.least_own)) * g.n_kv_heads * g.npb;
   }
+  p.pu = prefix_unit(g, p.prefix_len, p.least_own);  // without a prefix: no tiles
+  p.prefix_all = prefix_steps(g, p.pu) * g.n_kv_heads * g.npb;
   p.bad = __any_sync(0xffffffffu, bad);
   p.total = p.prefix_all + own;
   p.cs = chunk_begin(p.total, workers, c);
@@ -137,26 +137,23 @@ struct RowSegment {
 
 // Walks the segments of a chunk in order; every warp that needs them runs its own.
 struct RowSegments {
-  int32_t pos, ce, cs, prefix_all, y_start;
-  int32_t y;
-  UnitTiles pu;
+  const RowsPlan *plan;  // in shared memory, in the row kernel
+  int32_t pos, y_start, y;
 
-  __device__ __forceinline__ void init(const RowsGeom &g, const RowsPlan &p) {
-    pos = cs = p.cs;
-    ce = p.ce;
-    prefix_all = p.prefix_all;
+  __device__ __forceinline__ void init(const RowsPlan &p) {
+    plan = &p;
+    pos = p.cs;
     y_start = p.y_start;
     y = p.y;
-    pu = prefix_unit(g, p.prefix_len, p.least_own);
   }
 
   __device__ __forceinline__ bool next(const RowsGeom &g, RowSegment &s) {
-    const int32_t pairs = g.batch * g.nqb;
+    const int32_t pairs = g.batch * g.nqb, ce = plan->ce;
     while (pos < ce) {
-      if (pos < prefix_all) {
-        const int32_t steps = prefix_steps(g, pu);
+      if (pos < plan->prefix_all) {
+        const int32_t steps = prefix_steps(g, plan->pu);
         s.prefix = true;
-        s.u = pu;
+        s.u = plan->pu;
         s.unit = pos / steps;
         s.x = s.unit / g.npb;
         s.qb = s.unit - s.x * g.npb;
@@ -181,7 +178,7 @@ struct RowSegments {
         s.start = y_start + s.x * (s.u.n + g.unit_cost);
       }
       const int32_t first = s.start + g.unit_cost;  // its first tile's step
-      s.opens = s.start <= cs;
+      s.opens = s.start <= plan->cs;
       s.t0 = imax32(0, pos - first);
       s.t1 = imin32(ce - first, s.u.n);  // (negative: none)
       pos = imin32(first + s.u.n, ce);
@@ -252,10 +249,9 @@ __device__ __forceinline__ void write_pair_starts(const RowsGeom &g, const RowsP
   const int lane = threadIdx.x & 31;
   const int32_t pairs = g.batch * g.nqb;
   if (lane == 0) {
-    const UnitTiles pu = prefix_unit(g, p.prefix_len, p.least_own);
     entry->steps = p.total;
-    entry->prefix_steps = prefix_steps(g, pu);
-    entry->prefix_tiles = pu.n;
+    entry->prefix_steps = prefix_steps(g, p.pu);
+    entry->prefix_tiles = p.pu.n;
   }
   int32_t base = p.prefix_all;
   for (int32_t y0 = 0; y0 < pairs; y0 += 32) {

@@ -165,7 +165,7 @@ void check_case(std::mt19937_64 &rng, int k) {
       if (chunk_of(pl.total, workers, f) != c) fail("chunk_of", k);
     steps_done = pl.ce;
     RowSegments it;
-    it.init(g, pl);
+    it.init(pl);
     RowSegment s;
     int64_t last = -1;
     int segments = 0;

@@ -63,7 +63,7 @@ def test_row_planner(tmp_path):
      "s.first = partial_slot(false, c, 0, first <= begin);"),
     ("return static_cast<int32_t>(((static_cast<int64_t>(step) + 1) * n - 1) / steps);",
      "return static_cast<int32_t>(static_cast<int64_t>(step) * n / steps);"),
-    ("s.opens = s.start <= cs;", "s.opens = s.start < cs;"),
+    ("s.opens = s.start <= plan->cs;", "s.opens = s.start < plan->cs;"),
     ("if (y_start + span > pos) break;", "if (y_start + span >= pos) break;"),
 ])
 def test_planted_mistake_is_caught(tmp_path, original, planted):
