@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           }
           // The largest product (times the scale's sign: scale and soft-cap are monotonic).
           float best = -INFINITY;
+          float widest = 0.f;  // with a soft-cap: the largest magnitude, of any column
 #pragma unroll 1
           for (int ch = 0; ch < TILE / CW; ++ch) {
             float s[CW];
@@ -594,6 +595,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
               for (int c = 0; c < CW; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
             }
             best = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            if (CAP) {
+              float a4[4] = {widest, widest, widest, widest};
+#pragma unroll
+              for (int c = 0; c < CW; ++c) a4[c & 3] = fmaxf(a4[c & 3], fabsf(s[c]));
+              widest = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
+            }
           }
           if (NH == 2 && ok) {
             tmem_store_wait();
@@ -645,15 +652,23 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // fp32 before its own truncation): 2^-14 relative.  A row without any score
           // yet (reference -inf) has only masked columns here.
           const float mr = now == -INFINITY ? 0.f : now;
+          const bool small =
+              CAP && __all_sync(0xffffffffu, !row_ok || widest * fabsf(p.qscale) <= kSmallTanh);
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int ch = 0; ch < TILE / CW; ++ch) {
             float s[CW], w[CW];
             if (ok) tmem_load(s_col + CW * ch, s);
+            if (small) {
 #pragma unroll
-            for (int c = 0; c < CW; ++c)
-              s[c] = CAP ? ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr)
-                         : ex2_approx(fmaf(s[c], p.qscale, -mr));
+              for (int c = 0; c < CW; ++c)
+                s[c] = ex2_approx(small_score_log2(s[c], p.qscale, p.post) - mr);
+            } else {
+#pragma unroll
+              for (int c = 0; c < CW; ++c)
+                s[c] = CAP ? ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr)
+                           : ex2_approx(fmaf(s[c], p.qscale, -mr));
+            }
             if (masked) {
               const uint32_t bits = static_cast<uint32_t>(seen >> (CW * ch));
 #pragma unroll
@@ -750,44 +765,62 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           row_there |= __shfl_sync(0xffffffffu, row_ok ? 1u : 0u, (lane & ~3) + k) << k;
         }
         if (ok) tc_fence_after();
-        const bool few = nrow <= 8;  // rows of one warp: no line is worth the swap
-        const int units = final_rows ? DH / 64 : DH / 32;  // 128-byte lines of a row
+        if (nrow <= 8 && !final_rows && ok) {
+          // A few rows' pieces: no line is worth the swap, and reading 64 columns at a
+          // time leaves fewer waits.
 #pragma unroll 1
-        for (int u = 0; u < units; ++u) {
-          uint32_t v[32];
-          if (!ok) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = 0;
-          } else if (final_rows) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float o[32];
-              tmem_load32(tmem + lane_base + Cfg::O_COL + u * 64 + half * 32, o);
-#pragma unroll
-              for (int q = 0; q < 16; ++q)
-                v[16 * half + q] = pack_bf16x2(o[2 * q] * inv, o[2 * q + 1] * inv);
+          for (int u = 0; u < DH / 64; ++u) {
+            float o[64];
+            tmem_ld64(tmem + lane_base + Cfg::O_COL + u * 64, o);
+            if (u + 1 == DH / 64) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(oempty);
             }
-          } else {
-            float o[32];
-            tmem_load32(tmem + lane_base + Cfg::O_COL + u * 32, o);
+            if (row_ok) {
 #pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(o[q] * inv);
+              for (int k = 0; k < 8; ++k) {
+                uint32_t v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = __float_as_uint(o[8 * k + q] * inv);
+                st_global_v8(base + u * 256 + k * 32, v);
+              }
+            }
           }
-          if (u + 1 == units) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(oempty);
-          }
-          if (few) {
+        } else {
+          const int units = final_rows ? DH / 64 : DH / 32;  // 128-byte lines of a row
+#pragma unroll 1
+          for (int u = 0; u < units; ++u) {
+            uint32_t v[32];
+            if (!ok) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) v[q] = 0;
+            } else if (final_rows) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                float o[32];
+                tmem_load32(tmem + lane_base + Cfg::O_COL + u * 64 + half * 32, o);
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                  v[16 * half + q] = pack_bf16x2(o[2 * q] * inv, o[2 * q + 1] * inv);
+              }
+            } else {
+              float o[32];
+              tmem_load32(tmem + lane_base + Cfg::O_COL + u * 32, o);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(o[q] * inv);
+            }
+            if (u + 1 == units) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(oempty);
+            }
+            swap_pieces(v, lane);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (row_ok) st_global_v8(base + u * 128 + k * 32, v + 8 * k);
-            continue;
+              if ((row_there >> k) & 1)
+                st_global_v8(row_base[k] + u * 128 + (lane & 3) * 32, v + 8 * k);
           }
-          swap_pieces(v, lane);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((row_there >> k) & 1) st_global_v8(row_base[k] + u * 128 + (lane & 3) * 32, v + 8 * k);
         }
         if (row_ok && rank == 0) {
           const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
