@@ -102,9 +102,11 @@ __global__ void __launch_bounds__(kSlotMapThreads) slot_map_kernel(const SlotMap
       }
       seq = s_seq[a];
       const int32_t L = __ldg(p.seqlens + seq);
-      pos = L - imax32(0, __ldg(p.new_lens + seq)) + (i - s_start[a]);
+      // In 64 bits: a negative length under many new tokens leaves 32.
+      const int64_t at = static_cast<int64_t>(L) - __ldg(p.new_lens + seq) + (i - s_start[a]);
+      pos = static_cast<int32_t>(at > INT32_MIN ? at : INT32_MIN);
       // A row of the ring survives the step if no later position takes its slot.
-      if (pos >= 0 && (pos < p.sinks || pos >= L - (p.capacity - p.sinks)))
+      if (pos >= 0 && (pos < p.sinks || at >= static_cast<int64_t>(L) - (p.capacity - p.sinks)))
         slot = slot_of(pos, p.sinks, p.capacity);
     }
     p.row_seq[r0 + i] = seq;

@@ -39,9 +39,9 @@
 // and 8-11 run the softmax of even and of odd tiles.  Every wait is bounded.
 //
 // A parity wait is sound only while its barrier is in the phase waited for or the
-// next.  kfull, vfull: their eight uses back tile i - 8's products are done.  odone of tile j: Q.K of tile j waited for the use before it, and whoever
-// waits has seen tile j's scores; it cannot complete again before tile j + 4, which
-// needs the waiter's own weights.  refset: the two groups alternate inside a
+// next.  kfull, vfull: eight uses back, tile i - 8's products are done.  odone of tile
+// j: Q.K of tile j waited for the use before it, and whoever waits has seen tile j's
+// scores; it cannot complete again before tile j + 4, which needs the waiter's own weights.  refset: the two groups alternate inside a
 // segment and meet at its end.  oempty: a group arrives behind the segment's last
 // P.V, whose first one waited for the phase before.
 #pragma once
@@ -86,7 +86,8 @@ struct RowsParams {
   RowsGeom g;
   uint16_t *out;       // bf16 [T][B][Hq][D]
   float *lse;          // [T][B][Hq] or null
-  float *own_o, *own_lse;  // partials of own units, rs rows a slot
+  float *own_o, *own_lse;  // partials of own units, rs rows a slot; a CTA pair's two have
+  int64_t lse_stride;      // a copy of own_lse each, lse_stride elements apart
   float *pre_o, *pre_lse;  // partials of prefix units, rp rows a slot
   CutEntry *cuts;          // [workers - 1], a call without a prefix (null: the last piece's
                            // CTA joins a cut unit here, no merge kernel follows), and
@@ -272,8 +273,9 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------- tile loads
-    // Tiles without any of the step's own rows hold what earlier steps wrote and are
-    // loaded before the kernel in front has ended.
+    // Tiles of a sequence's cache without any of the step's own rows hold what earlier
+    // steps wrote and are loaded before the kernel in front has ended.  A prefix may be
+    // another sequence's cache, to which the call in front appends: its tiles wait.
     bool waited = false;
     const uint64_t pol = l2_evict_first_policy();
     bool ok = true;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       if (e >= NST) ok = mbar_wait(&empty[st], ((e / NST) - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      if (!waited && !sg.prefix && tile.pos + tile.ntok > sg.L - g.tokens) {
+      if (!waited && (sg.prefix || tile.pos + tile.ntok > sg.L - g.tokens)) {
         grid_dependency_wait();
         waited = true;
       }
@@ -822,10 +824,14 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
                 st_global_v8(row_base[k] + u * 128 + (lane & 3) * 32, v + 8 * k);
           }
         }
-        if (row_ok && rank == 0) {
-          const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
-          if (!final_rows)
-            (seg.prefix ? p.pre_lse : p.own_lse)[prow] = lse2;
+        const float lse2 = l > 0.f ? m_ref + log2f(l) : -INFINITY;
+        if (row_ok && !seg.prefix && !final_rows) {
+          // Both CTAs of a pair: the CTA that joins a cut unit's pieces has counted the
+          // CTAs of its own rank, so it may read only what those wrote.
+          p.own_lse[rank * p.lse_stride + prow] = lse2;
+        } else if (row_ok && rank == 0) {
+          if (seg.prefix)
+            p.pre_lse[prow] = lse2;
           else if (p.lse != nullptr)
             p.lse[orow] = l > 0.f ? lse2 * kLn2 : -INFINITY;
         }
@@ -855,7 +861,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             const int32_t rq = row / g.group, rh = row - rq * g.group;
             const int64_t to = (static_cast<int64_t>(seg.qb * g.qt_seq + rq) * g.batch + seg.b) * Hq +
                                seg.x * g.group + rh;
-            join_pieces<Cfg::D>(p.own_o + rank * DH, p.own_lse, at, p.rs, row,
+            join_pieces<Cfg::D>(p.own_o + rank * DH, p.own_lse + rank * p.lse_stride, at, p.rs, row,
                                 p.out + to * Cfg::D + rank * DH,
                                 p.lse != nullptr && rank == 0 ? p.lse + to : nullptr);
           }

@@ -132,6 +132,7 @@ struct RowsLayout {
   RowsGeom g = {};
   int nh = 1, workers = 0;
   int32_t rs = 0, rp = 0;
+  int64_t lse_stride = 0;
   size_t table = 0, own_o = 0, own_lse = 0, pre_o = 0, pre_lse = 0, bytes = 0;
 };
 
@@ -186,7 +187,8 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
       prefix_rows > 0 ? 256 + (static_cast<size_t>(batch) * g.nqb + 1) * sizeof(int32_t)
                       : static_cast<size_t>(lay.workers) * sizeof(CutEntry);
   lay.own_lse = align256(lay.table + table_bytes);
-  lay.pre_lse = align256(lay.own_lse + own_rows * 4);
+  lay.lse_stride = static_cast<int64_t>(own_rows);
+  lay.pre_lse = align256(lay.own_lse + lay.nh * own_rows * 4);
   lay.own_o = align256(lay.pre_lse + pre_rows * 4);
   lay.pre_o = align256(lay.own_o + own_rows * d->head_dim * 4);
   lay.bytes = align256(lay.pre_o + pre_rows * d->head_dim * 4);
@@ -250,6 +252,7 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   p.lse = lse;
   p.own_o = reinterpret_cast<float *>(ws + lay.own_o);
   p.own_lse = reinterpret_cast<float *>(ws + lay.own_lse);
+  p.lse_stride = lay.lse_stride;
   p.pre_o = reinterpret_cast<float *>(ws + lay.pre_o);
   p.pre_lse = reinterpret_cast<float *>(ws + lay.pre_lse);
   // A block of few rows is joined by the row kernel itself; with more rows the four warps
@@ -292,13 +295,13 @@ gdattn_status check_write_args(const void *k_rows, const void *v_rows, int64_t r
                                const int32_t *row_seq, const int32_t *row_slot, int32_t n_rows,
                                int32_t batch, const gdattn_layer_desc *desc, const void *k_cache,
                                const void *v_cache) {
-  if (desc == nullptr || k_cache == nullptr || k_rows == nullptr || row_seq == nullptr ||
-      row_slot == nullptr)
-    return GDATTN_ERR_INVALID_ARG;
+  if (desc == nullptr || k_cache == nullptr) return GDATTN_ERR_INVALID_ARG;
   gdattn_status st = check_desc(desc);
   if (st != GDATTN_OK) return st;
-  if ((desc->kv_shared == 1) != (v_cache == nullptr) ||
-      (desc->kv_shared == 1) != (v_rows == nullptr))
+  if ((desc->kv_shared == 1) != (v_cache == nullptr)) return GDATTN_ERR_INVALID_ARG;
+  // Without rows there is nothing to point at.
+  if (n_rows != 0 && (k_rows == nullptr || row_seq == nullptr || row_slot == nullptr ||
+                      (desc->kv_shared == 1) != (v_rows == nullptr)))
     return GDATTN_ERR_INVALID_ARG;
   if (n_rows < 0 || batch <= 0 ||
       row_stride < static_cast<int64_t>(desc->n_kv_heads) * desc->head_dim || row_stride % 8 != 0)

@@ -332,6 +332,11 @@ gdattn_status gdattn_decode_multi(const void *q, const void *k_cache, const void
  * gdattn_workspace_init, at least as large as the largest size asked for) may
  * serve them and the calls above in turn.  GDATTN_FLAG_EVEN_UNITS has no
  * effect here: the planner always evens the work out from the device's lengths.
+ *
+ * Before the preceding kernel has completed (see the conventions) the two
+ * attention calls read only seqlens, prefix_len and the rows of the sequences' own
+ * caches that belong to positions below L_b - T.  The prefix rows, like q, are read
+ * after it: the call in front may have appended to them.
  */
 
 /*
@@ -419,7 +424,8 @@ gdattn_status gdattn_decode_prefix(const void *q, const void *k_prefix, const vo
  *  row_pos    int32 [n_rows]: its position in the sequence
  *  row_slot   int32 [n_rows]: its slot in the sequence's cache, or -1 when a later
  *             row of the same step takes that slot (a prompt longer than the
- *             ring), or when the position is negative (new_lens above seqlens)
+ *             ring), or when the position is negative (new_lens above seqlens;
+ *             positions below -2^31 read as that)
  */
 gdattn_status gdattn_slot_map(const int32_t *seqlens, const int32_t *new_lens, int32_t batch,
                               int32_t n_rows, int32_t cache_capacity, int32_t n_sink,
@@ -434,10 +440,12 @@ gdattn_status gdattn_slot_map(const int32_t *seqlens, const int32_t *new_lens, i
  * of them there, piecewise; a slot map has no such rows.
  *
  *  k_rows      bf16, row i at k_rows + i * row_stride elements: [Hkv][D], the
- *              heads next to one another (a slice of a fused projection)
+ *              heads next to one another (a slice of a fused projection); the
+ *              rows must not overlap the caches
  *  v_rows      the same, or NULL when desc->kv_shared == 1
  *  row_stride  >= Hkv * D and a multiple of 8
- *  row_seq, row_slot   int32 [n_rows], device; n_rows may be 0
+ *  row_seq, row_slot   int32 [n_rows], device; n_rows may be 0 (the rows' pointers
+ *              and these are then not looked at, and nothing is launched)
  *  desc        geometry, capacity and cache_batch_stride; window, scale, softcap
  *              and flags are checked but not used
  *  k_cache, v_cache    as gdattn_decode's, written

@@ -545,3 +545,71 @@ def test_fp8_rows_written_here_are_what_the_fp8_decode_reads():
     # the entry point's own gates
     assert (out.cpu().double() - torch.as_tensor(o_ref)).abs().max() <= 8e-3
     assert (lse.cpu().double() - torch.as_tensor(l_ref)).abs().max() <= 1e-3
+
+
+# ------------------------------------------- what one call leaves for the next
+def test_pieces_of_a_pair_are_joined_from_this_call():
+    """head_dim 512, few rows: each CTA of a pair joins its half of the dims from pieces
+    and sums of this call, not of the one before on the same workspace."""
+    args = dict(T=1, window=2500, sinks=4, hq=16, hkv=1, dim=512, shared=True)
+    calls = [Call(ref.make_case(k, lens=lens, capacity=2504, q_scale=4.0 + 8 * k, **args),
+                  max_seqlen=4000) for k, lens in enumerate(([3000, 2600], [900, 2700]))]
+    want = [tuple(t.clone() for t in call.run()) for call in calls]
+    for call, w in zip(calls, want):
+        ref.check(*w, ref.reference(call.c, "cuda"))
+        call.ws.t = calls[0].ws.t
+    got = []
+    for _ in range(100):
+        for call in calls:
+            call.enqueue()
+            got.append((call.out.t.clone(), call.lse.t.clone()))
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
+
+
+def test_a_prefix_that_the_call_in_front_appends_to():
+    """Sequence 0's cache serves as the others' prefix right behind its own append."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    hq, dim, P, B = 16, 512, 4000, 3
+    desc = binding.make_desc(hq, 1, dim, 0, 0.0, dim ** -0.5, True, P)
+    cache, own = normal(1, P, 1, dim), normal(B, P, 1, dim)
+    plen = torch.tensor([P], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([5, 1, 70], dtype=torch.int32, device="cuda")
+    q0, q = normal(1, hq, dim), normal(1, B, hq, dim)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda")
+          for n in (binding.workspace_size(1, P, desc),
+                    binding.prefix_workspace_size(B, 1, 100, P, desc))]
+    for w in ws:
+        binding.workspace_init(w)
+
+    def behind():
+        return binding.decode_prefix(q, cache[0], None, plen, own, None, lens, desc, 100,
+                                     workspace=ws[1])[0]
+
+    for _ in range(20):
+        new = normal(1, 1, dim) * 8
+        binding.decode_append(q0, new, None, cache, None, plen, desc, P, workspace=ws[0])
+        got = behind()
+        torch.cuda.synchronize()
+        assert torch.equal(cache[0, P - 1], new[0])
+        assert torch.equal(got, behind())
+
+
+def test_new_rows_far_above_a_length():
+    """Positions below -2^31 read as that; no row has a slot."""
+    m = binding.slot_map(dev(i32([-5, 9])), dev(i32([2 ** 31 - 1, 2])), 4, 8, 2)
+    assert m.pos.tolist() == [-2 ** 31] * 4 and m.slot.tolist() == [-1] * 4
+    assert m.seq.tolist() == [0] * 4 and m.start.tolist() == [0, 2 ** 31 - 1, 2 ** 31 - 1]
+
+
+def test_a_step_without_rows():
+    desc = binding.make_desc(16, 8, 256, 0, 0.0, 1.0, False, 8)
+    kv = torch.ones((2, 1, 8, 8, 256), device="cuda").to(torch.bfloat16)
+    rows = torch.zeros((0, 32, 256), dtype=torch.bfloat16, device="cuda")
+    at = torch.zeros(0, dtype=torch.int32, device="cuda")
+    binding.cache_write(rows[:, 16:24], rows[:, 24:], at, at, desc, kv[0], kv[1])
+    assert (kv == 1).all()

@@ -165,6 +165,16 @@ def test_no_rows_is_no_launch():
     assert write_fp8(n=0) == binding.GDATTN_OK
 
 
+@pytest.mark.parametrize("call", [write, write_fp8])
+def test_no_rows_need_no_pointers(call):
+    """What a tensor without elements points at is null."""
+    none = dict(k=None, v=None, seq=None, slot=None)
+    assert call(n=0, **none) == binding.GDATTN_OK
+    assert call(n=0, kc=None, **none) == INVALID
+    assert call(n=0, vc=None, **none) == INVALID
+    assert call(n=1, k=A, v=None) == INVALID
+
+
 # ------------------------------------------------- the binding's tensor checks
 @pytest.fixture
 def any_device(monkeypatch):
