@@ -41,9 +41,16 @@
 // A parity wait is sound only while its barrier is in the phase waited for or the
 // next.  kfull, vfull: eight uses back, tile i - 8's products are done.  odone of tile
 // j: Q.K of tile j waited for the use before it, and whoever waits has seen tile j's
-// scores; it cannot complete again before tile j + 4, which needs the waiter's own weights.  refset: the two groups alternate inside a
-// segment and meet at its end.  oempty: a group arrives behind the segment's last
-// P.V, whose first one waited for the phase before.
+// scores; it cannot complete again before tile j + 4, which needs the waiter's own
+// weights.  refset: the two groups alternate inside a segment and meet at its end.
+// oempty: a group arrives behind the segment's last P.V, whose first one waited for
+// the phase before.
+//
+// Warp 0 finds the segments and passes them on in eight slots, without waiting for
+// their readers: it writes segment n + 8 in front of loading that segment's first tile
+// i, and to load tile i - 1 it waited for the products of tile i - 6 (or a later one).
+// Tiles i - 7 and i - 6 come behind segment n's first tile, so both softmax groups,
+// and with them every other warp, have read segment n.
 #pragma once
 
 #include <cstdint>
@@ -182,9 +189,19 @@ __device__ __forceinline__ void join_pieces(const float *o, const float *lse, co
   if (lane == 0 && out_lse != nullptr) *out_lse = z > 0.f ? (m + log2f(z)) * kLn2 : -INFINITY;
 }
 
+// Segment n of a chunk, found again from its start; for a warp whose loader gave up.
+__device__ __noinline__ bool nth_segment(const RowsGeom *g, const RowsPlan *plan, uint32_t n,
+                                         RowSegment *s) {
+  RowSegments it;
+  it.init(*plan);
+  for (uint32_t k = 0; k <= n; ++k)
+    if (!it.next(*g, *s)) return false;
+  return true;
+}
+
 template <int NH, bool SHARED, bool CAP>
 __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
-    rows_attn_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
+    rows_attn_kernel(const __grid_constant__ RowsMaps maps, const __grid_constant__ RowsParams p) {
   using Cfg = RowsConfig<NH>;
   constexpr int DH = Cfg::DH, NST = Cfg::NST, TILE = Cfg::TILE, CW = Cfg::CW;
 
@@ -213,7 +230,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   uint32_t *tmem_base_smem = reinterpret_cast<uint32_t *>(bars + 64);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 65);
   RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 66);
-  volatile int *last_piece = reinterpret_cast<volatile int *>(bars + 100);  // [2 groups]
+  static_assert(sizeof(RowsPlan) <= 9 * 8, "the plan's place");
+  volatile int *last_piece = reinterpret_cast<volatile int *>(bars + 75);  // [2 groups]
+  uint64_t *seg_full = bars + 76;  // [8] warp 0 -> everyone: segment n & 7 is there
+  constexpr uint32_t kSlots = 8;
+  int32_t *seg_slots = reinterpret_cast<int32_t *>(bars + 84);  // [8][kSegmentWords]
+  static_assert(84 * 8 + kSlots * kSegmentWords * 4 <= 1024, "barriers and segments");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -235,6 +257,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     }
     mbar_init(oempty, 4);
     for (int s = 0; s < 8; ++s) {
+      mbar_init(&seg_full[s], 1);
       mbar_init(&kfull[s], 1);
       mbar_init(&vfull[s], 1);
       mbar_init(&refset[s], 1);
@@ -267,9 +290,21 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_base_smem;
   const RowsPlan &plan = *plan_smem;
-  RowSegments segs;
-  segs.init(plan);
   RowSegment seg;
+  // Segment n (false: there is none), by a whole warp.
+  auto take = [&](uint32_t n) {
+    const bool there =
+        mbar_wait(&seg_full[n % kSlots], (n / kSlots) & 1, abort_flag, p.status);
+    if (__all_sync(0xffffffffu, there)) {
+      unpack_segment(g, seg_slots + n % kSlots * kSegmentWords, seg);
+      return seg.t1 > seg.t0;
+    }
+    // Every warp walks all segments, whatever failed: the groups' barriers stay paired.
+    RowSegment found = {};
+    const bool any = nth_segment(&p.g, plan_smem, n, &found);
+    seg = found;
+    return any;
+  };
 
   if (warp == 0) {
     // --------------------------------------------------------- tile loads
@@ -314,23 +349,38 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       __syncwarp();
       ++(is_v ? nv : nk);
     };
+    RowSegments segs;
+    segs.init(plan);
+    uint32_t n = 0;  // segments passed on
+    auto next = [&]() {
+      if (!ok) return false;
+      const bool any = segs.next(g, seg);
+      if (!any) seg = RowSegment{};  // tells the end: a segment of no tiles
+      if (lane == 0) {
+        pack_segment(seg, seg_slots + n % kSlots * kSegmentWords);
+        mbar_arrive(&seg_full[n % kSlots]);
+      }
+      __syncwarp();
+      ++n;
+      return any;
+    };
     if (SHARED) {
-      while (ok && segs.next(g, seg))
+      while (next())
         for (int32_t t = seg.t0; ok && t < seg.t1; ++t) load(seg, t, false);
     } else {
       // K tiles run kAhead tiles in front of V tiles: a V tile is needed only after
       // its scores' softmax, and its slot is better used by a K tile until then.
-      RowSegments vsegs = segs;
       RowSegment vseg = {};
       int32_t vt = 0;
+      uint32_t vn = 0;
       auto load_v = [&]() {
-        if (nv == 0 || vt == vseg.t1) {
-          vsegs.next(g, vseg);
+        if (vt == vseg.t1) {  // (at most kAhead segments behind the K tiles')
+          unpack_segment(g, seg_slots + vn++ % kSlots * kSegmentWords, vseg);
           vt = vseg.t0;
         }
         load(vseg, vt++, true);
       };
-      while (ok && segs.next(g, seg))
+      while (next())
         for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
           load(seg, t, false);
           if (ok && nk > Cfg::kAhead) load_v();
@@ -346,14 +396,14 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q loads
     grid_dependency_wait();
+    bool has = take(0);
     if (rank == 0) {
       if (plan.bad && worker == 0 && lane == 0) atomicOr(p.status, kStatusSeqlen);
       if (g.prefix_len != nullptr) {
         if (worker == 0) write_pair_starts(g, plan, p.prefix_entry, p.pair_start);
       } else if (p.cuts != nullptr && worker > 0 && lane == 0) {
-        RowSegments it = segs;
         CutEntry cut = {};
-        if (it.next(g, seg) &&
+        if (has &&
             cut_parts(plan.total, p.workers, worker - 1, seg.start, g.unit_cost, seg.u.n,
                       cut.parts)) {
           cut.b = seg.b;
@@ -368,7 +418,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     }
     bool ok = true;
     uint32_t n = 0;  // blocks so far
-    while (ok && segs.next(g, seg)) {
+    while (ok && has) {
       const uint32_t buf = n % p.q_bufs, use = n / p.q_bufs;
       if (use > 0) ok = mbar_wait(&qempty[buf], (use - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
@@ -387,7 +437,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
         }
       }
       __syncwarp();
-      ++n;
+      has = take(++n);
     }
     volatile int no_abort = 0;
     const uint32_t bufs = static_cast<uint32_t>(p.q_bufs);
@@ -400,7 +450,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     const uint64_t kdesc = smem_desc_sw128(smem_u32(kv), 16, 1024);  // K-major
     bool ok = true;
     uint32_t i = 0, n = 0;
-    while (ok && segs.next(g, seg)) {
+    while (ok && take(n)) {
       const uint32_t buf = n % p.q_bufs, use = n / p.q_bufs;
       ok = mbar_wait(&qfull[buf], use & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
@@ -440,7 +490,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     const uint64_t vdesc = smem_desc_sw128(smem_u32(kv), Cfg::BOXB, 1024);
     bool ok = true;
     uint32_t i = 0, n = 0;
-    for (; ok && segs.next(g, seg); ++n) {
+    for (; ok && take(n); ++n) {
       for (int32_t t = seg.t0; ok && t < seg.t1; ++t) {
         const int st = v_entry<NH, SHARED>(i) % NST, pb = i & 3;
         // The first product of a block overwrites O: its last block was read.
@@ -486,6 +536,8 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     float *ref_own = ref + wg * Cfg::M + r, *ref_other = ref + (wg ^ 1) * Cfg::M + r;
     uint64_t *set_own = &refset[wg * 4 + qd], *set_other = &refset[(wg ^ 1) * 4 + qd];
     const float sign = p.qscale >= 0.f ? 1.f : -1.f;
+    const float2x qscale2 = pack2(p.qscale, p.qscale), minus_one = pack2(-1.f, -1.f);
+    const SmallTanh small_tanh(p.qscale, p.post);
     bool ok = true;
     uint32_t i = 0;       // tiles so far
     uint32_t n_own = 0;   // references this warp set
@@ -497,12 +549,12 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       if (lent) pair_sync(5 + qd);
       lent = false;
     };
-    while (segs.next(g, seg)) {
+    const int32_t tq = r / g.group, h = r - tq * g.group;  // the row's token and head
+    for (uint32_t n = 0; take(n); ++n) {
       // The row: its token, sequence and head, and the positions it sees.
       const int32_t qt = seg.prefix ? g.qt_pre : g.qt_seq;
       const int32_t all = seg.prefix ? g.tokens * g.batch : g.tokens;  // of this axis
       const int32_t nrow = imin32(qt, all - seg.qb * qt) * g.group;
-      const int32_t tq = r / g.group, h = r - tq * g.group;
       const bool row_ok = r < nrow;
       RowRange rg = {0, 0, 0};
       if (row_ok) {
@@ -556,6 +608,14 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
             }
             ok = __all_sync(0xffffffffu, ok);
           }
+          auto walk = [&](auto &&f) {  // f(chunk, its CW scores)
+#pragma unroll 1
+            for (int ch = 0; ch < TILE / CW; ++ch) {
+              float s[CW];
+              if (ok) tmem_load(s_col + CW * ch, s);
+              f(ch, s);
+            }
+          };
           // Column c is position tile.pos + c; bit c of `seen` says whether the row sees
           // it.  A tile that every row of the warp sees in full needs no mask.  (Lanes
           // without a row may compute anything: nothing of it is stored.)
@@ -570,10 +630,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           // The largest product (times the scale's sign: scale and soft-cap are monotonic).
           float best = -INFINITY;
           float widest = 0.f;  // with a soft-cap: the largest magnitude, of any column
-#pragma unroll 1
-          for (int ch = 0; ch < TILE / CW; ++ch) {
-            float s[CW];
-            if (ok) tmem_load(s_col + CW * ch, s);
+          auto scan = [&](int ch, float (&s)[CW]) {
             if (NH == 2 && ok) {
               const float4 *x = xs + wg * (Cfg::XB / 16) + ch * (CW / 4) * Cfg::M + r;
 #pragma unroll
@@ -586,24 +643,31 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
               }
               tmem_store(s_col + CW * ch, s);
             }
-            const uint32_t bits = static_cast<uint32_t>(seen >> (CW * ch));
             float m4[4] = {best, best, best, best};
             if (masked) {
+              const uint32_t bits = static_cast<uint32_t>(seen >> (CW * ch));
 #pragma unroll
               for (int c = 0; c < CW; ++c)
                 m4[c & 3] = fmaxf(m4[c & 3], (bits >> c) & 1 ? s[c] * sign : -INFINITY);
+            } else if (sign > 0.f) {
+#pragma unroll
+              for (int c = 0; c < CW; c += 2)
+                m4[c / 2 & 3] = max3(m4[c / 2 & 3], s[c], s[c + 1]);
             } else {
 #pragma unroll
-              for (int c = 0; c < CW; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c] * sign);
+              for (int c = 0; c < CW; c += 2)
+                m4[c / 2 & 3] = -min3(-m4[c / 2 & 3], s[c], s[c + 1]);
             }
             best = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             if (CAP) {
               float a4[4] = {widest, widest, widest, widest};
 #pragma unroll
-              for (int c = 0; c < CW; ++c) a4[c & 3] = fmaxf(a4[c & 3], fabsf(s[c]));
+              for (int c = 0; c < CW; c += 2)
+                a4[c / 2 & 3] = max3(a4[c / 2 & 3], fabsf(s[c]), fabsf(s[c + 1]));
               widest = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
             }
-          }
+          };
+          walk(scan);
           if (NH == 2 && ok) {
             tmem_store_wait();
             __syncwarp();
@@ -656,42 +720,49 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           const float mr = now == -INFINITY ? 0.f : now;
           const bool small =
               CAP && __all_sync(0xffffffffu, !row_ok || widest * fabsf(p.qscale) <= kSmallTanh);
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int ch = 0; ch < TILE / CW; ++ch) {
-            float s[CW], w[CW];
-            if (ok) tmem_load(s_col + CW * ch, s);
-            if (small) {
+          const float2x minus_mr = pack2(-mr, -mr);
+          float2x l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+          auto weigh = [&](int ch, float (&s)[CW]) {
+            if (CAP && !small) {
 #pragma unroll
               for (int c = 0; c < CW; ++c)
-                s[c] = ex2_approx(small_score_log2(s[c], p.qscale, p.post) - mr);
+                s[c] = ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr);
             } else {
 #pragma unroll
-              for (int c = 0; c < CW; ++c)
-                s[c] = CAP ? ex2_approx(score_log2<CAP>(s[c], p.qscale, p.post) - mr)
-                           : ex2_approx(fmaf(s[c], p.qscale, -mr));
+              for (int c = 0; c < CW; c += 2) {
+                const float2x x = pack2(s[c], s[c + 1]);
+                float ea, eb;
+                unpack2(CAP ? small_tanh(x, minus_mr) : fma2(x, qscale2, minus_mr), ea, eb);
+                s[c] = ex2_approx(ea);
+                s[c + 1] = ex2_approx(eb);
+              }
             }
             if (masked) {
               const uint32_t bits = static_cast<uint32_t>(seen >> (CW * ch));
 #pragma unroll
               for (int c = 0; c < CW; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
             }
+            float w[CW];
 #pragma unroll
             for (int j = 0; j < CW / 2; ++j) {
-              const float pa = s[2 * j], pb = s[2 * j + 1];
-              l4[j & 3] += pa + pb;
-              const uint32_t ua = __float_as_uint(pa), ub = __float_as_uint(pb);
-              const float ra = pa - __uint_as_float(ua & 0xFFFF0000u);
-              const float rb = pb - __uint_as_float(ub & 0xFFFF0000u);
-              const int at = j / 8 * 16 + j % 8;  // 8 columns of weights, 8 of remainders
-              w[at] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
-              w[at + 8] =
-                  __uint_as_float(__byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
+              const uint32_t ua = __float_as_uint(s[2 * j]), ub = __float_as_uint(s[2 * j + 1]);
+              const float2x pw = pack2(s[2 * j], s[2 * j + 1]);
+              l2[j & 1] = add2(l2[j & 1], pw);
+              const float2x hi = pack2(__uint_as_float(ua & 0xFFFF0000u),
+                                       __uint_as_float(ub & 0xFFFF0000u));
+              float ra, rb;
+              unpack2(fma2(hi, minus_one, pw), ra, rb);
+              w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));  // 8 columns of weights,
+              w[j + 8] = __uint_as_float(                           // 8 of remainders
+                  __byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
             }
             if (ok) tmem_store(s_col + CW * ch, w);
-          }
+          };
+          walk(weigh);
           if (ok) tmem_store_wait();
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          float la, lb;
+          unpack2(add2(l2[0], l2[1]), la, lb);
+          l += la + lb;
         }
         if (ok && tile.ntok < TILE) {
           // Rows behind the tile's end hold other slots, or what the ring held

@@ -188,6 +188,46 @@ struct RowSegments {
   }
 };
 
+// A segment as it passes between the warps of the row kernel, which find it once:
+// eight warps that each walked the units spent 5000 cycles a segment on it.
+constexpr int kSegmentWords = 11;
+
+GDATTN_HD void pack_segment(const RowSegment &s, int32_t *w) {
+  w[0] = s.x | (s.prefix ? 1 << 30 : 0) | (s.opens ? 1 << 29 : 0);  // (x is below 2^23)
+  w[1] = s.u.lo;
+  w[2] = s.u.slot0;
+  w[3] = s.u.run0;
+  w[4] = s.u.run1;
+  w[5] = s.t0;
+  w[6] = s.t1;
+  w[7] = s.b;
+  w[8] = s.qb;
+  w[9] = s.L;
+  w[10] = s.start;
+}
+
+GDATTN_HD void unpack_segment(const RowsGeom &g, const int32_t *w, RowSegment &s) {
+  s.x = w[0] & ((1 << 29) - 1);
+  s.prefix = (w[0] >> 30 & 1) != 0;
+  s.opens = (w[0] >> 29 & 1) != 0;
+  s.u.lo = w[1];
+  s.u.slot0 = w[2];
+  s.u.run0 = w[3];
+  s.u.run1 = w[4];
+  s.t0 = w[5];
+  s.t1 = w[6];
+  s.b = w[7];
+  s.qb = w[8];
+  s.L = w[9];
+  s.start = w[10];
+  s.u.pin = s.prefix ? 0 : imin32(g.sinks, s.u.lo);
+  s.u.slot1 = s.prefix ? 0 : g.sinks;
+  s.u.npin = tiles_of(s.u.pin);
+  s.u.n0 = tiles_of(s.u.run0);
+  s.u.n = s.prefix ? s.u.n0 : imax32(1, s.u.npin + s.u.n0 + tiles_of(s.u.run1));
+  s.unit = s.prefix ? s.x * g.npb + s.qb : (s.b * g.nqb + s.qb) * g.n_kv_heads + s.x;
+}
+
 // ---------------------------------------------------------------- partials
 // Slot of a segment's partial.  With a prefix every segment leaves one: chunk c
 // touching unit u of its kind writes slot c + u (if a later chunk touches unit u',

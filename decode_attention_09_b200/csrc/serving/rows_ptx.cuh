@@ -42,6 +42,25 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16 columns; tmem_load_wait before v is read.
+__device__ __forceinline__ void tmem_load16_start(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Names the registers, so that nothing reads them in front of the wait.
+__device__ __forceinline__ void tmem_load_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
+}
+
 // 32 of them.
 __device__ __forceinline__ void tmem_store32(uint32_t taddr, const float (&v)[32]) {
   uint32_t r[32];
@@ -145,18 +164,65 @@ __device__ __forceinline__ float score_log2(float s, float qscale, float post) {
   return fmaf(__fdividef(-2.f, e + 1.f), post, post);
 }
 
-// The same for |s qscale| <= kSmallTanh by tanh's Taylor series, whose first term left
-// out, 1382 / 155925 x^11, is below 2^-28 there.  No exponential and no division: the
+// For |s qscale| <= kSmallTanh tanh's Taylor series is used, whose first term left out,
+// 1382 / 155925 x^11, is below 2^-28 there.  No exponential and no division: the
 // capped weights of a tile take half the time.
 constexpr float kSmallTanh = 0.25f;
-__device__ __forceinline__ float small_score_log2(float s, float qscale, float post) {
-  const float x = s * qscale, y = x * x;
-  float t = fmaf(y, 62.f / 2835.f, -17.f / 315.f);
-  t = fmaf(y, t, 2.f / 15.f);
-  t = fmaf(y, t, -1.f / 3.f);
-  const float u = x * post;
-  return fmaf(u * y, t, u);
+
+// Two fp32 numbers that one instruction works on (half the issue slots of the softmax).
+using float2x = uint64_t;
+__device__ __forceinline__ float2x pack2(float a, float b) {
+  float2x r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ void unpack2(float2x v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ float2x fma2(float2x a, float2x b, float2x c) {
+  float2x r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float2x mul2(float2x a, float2x b) {
+  float2x r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2x add2(float2x a, float2x b) {
+  float2x r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest, or smallest, of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// cap log2(e) tanh(x) - mr by the series, x = s qscale; k are the series' factors of
+// x^3 to x^9 times post = cap log2(e).
+struct SmallTanh {
+  float2x qscale, post, k3, k5, k7, k9;
+  __device__ __forceinline__ SmallTanh(float q, float cap_log2e)
+      : qscale(pack2(q, q)),
+        post(pack2(cap_log2e, cap_log2e)),
+        k3(pack2(-1.f / 3.f * cap_log2e, -1.f / 3.f * cap_log2e)),
+        k5(pack2(2.f / 15.f * cap_log2e, 2.f / 15.f * cap_log2e)),
+        k7(pack2(-17.f / 315.f * cap_log2e, -17.f / 315.f * cap_log2e)),
+        k9(pack2(62.f / 2835.f * cap_log2e, 62.f / 2835.f * cap_log2e)) {}
+  __device__ __forceinline__ float2x operator()(float2x s, float2x minus_mr) const {
+    const float2x x = mul2(s, qscale), y = mul2(x, x);
+    const float2x g = mul2(y, fma2(y, fma2(y, fma2(y, k9, k7), k5), k3));
+    return fma2(x, g, fma2(x, post, minus_mr));
+  }
+};
 
 // --------------------------------------------- distributed shared memory
 // All threads of the cluster's CTAs; orders their earlier shared-memory accesses.

@@ -175,6 +175,18 @@ void check_case(std::mt19937_64 &rng, int k) {
       if (from < pl.cs || to > pl.ce || from <= last) fail("a segment outside its chunk", k);
       last = from;
       if (s.opens != (segments == 0)) fail("opens", k);
+      int32_t words[kSegmentWords];
+      pack_segment(s, words);
+      RowSegment w = {};
+      unpack_segment(g, words, w);
+      if (w.x != s.x || w.b != s.b || w.qb != s.qb || w.unit != s.unit || w.L != s.L ||
+          w.start != s.start || w.t0 != s.t0 || w.t1 != s.t1 || w.prefix != s.prefix ||
+          w.opens != s.opens || w.u.n != s.u.n)
+        fail("a packed segment", k);
+      for (int32_t t = s.t0; t < s.t1; ++t) {
+        const RowTile x = unit_tile(s.u, t), y = unit_tile(w.u, t);
+        if (x.pos != y.pos || x.slot != y.slot || x.ntok != y.ntok) fail("a packed tile", k);
+      }
       if (segments++ == 0) {
         first_of[c] = s;
         has_first[c] = true;
