@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   constexpr int DH = Cfg::DH, NST = Cfg::NST, TILE = Cfg::TILE, CW = Cfg::CW;
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+  // By an offset: the compiler then knows that these are shared addresses of 32 bits.
+  uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint8_t *qs = smem;
   uint8_t *kv = smem + Cfg::OFF_KV;
   // [2 groups][16 column quads][128 rows]

@@ -337,6 +337,9 @@ gdattn_status gdattn_decode_multi(const void *q, const void *k_cache, const void
  * attention calls read only seqlens, prefix_len and the rows of the sequences' own
  * caches that belong to positions below L_b - T.  The prefix rows, like q, are read
  * after it: the call in front may have appended to them.
+ *
+ * Slots that none of a step's tokens attends may hold anything.  A row that one of
+ * them attends has to be finite for the others too: a weight of 0 times NaN is NaN.
  */
 
 /*
