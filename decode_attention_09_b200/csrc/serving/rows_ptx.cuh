@@ -13,6 +13,12 @@ namespace gdattn {
 constexpr float kRefStep = 24.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
 // A box of query rows: 64 dims of consecutive heads of consecutive tokens.
 __device__ __forceinline__ void tma_load_tokens(void *dst_smem, const CUtensorMap *map, int32_t d,
                                                 int32_t head, int32_t token, uint64_t *bar) {

@@ -155,10 +155,11 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
   g.qt_pre = pairs < per_block ? pairs : per_block;
   g.npb = (pairs + g.qt_pre - 1) / g.qt_pre;
   lay.rs = g.qt_seq * g.group;
-  // A unit's start and end cost about as much as three of its tiles where the block is
-  // full (117 tiles in 37 units took 312 us on one CTA, in 7 units 190 us), and about
-  // one where it holds a few rows.
-  g.unit_cost = lay.rs > 32 ? 3 : 1;
+  // What a unit costs besides its tiles, in tiles.  Full blocks: three (one: prompt of
+  // 8192 tokens 307 us, three: 278; 512 question tokens 364 and 328).  A few rows: two
+  // (decode at batch 8 23.7 -> 22.8 us), or one where every piece goes to the merge anyway
+  // (4 sequences behind a prefix 23.4 -> 22.6).
+  g.unit_cost = lay.rs > 32 ? 3 : prefix_rows > 0 ? 1 : 2;
   lay.rp = g.qt_pre * g.group;
   const int64_t own_units = static_cast<int64_t>(batch) * g.nqb * g.n_kv_heads;
   // The kernels count steps in 32 bits.
