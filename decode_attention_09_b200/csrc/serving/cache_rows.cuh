@@ -33,7 +33,8 @@ constexpr int kSlotMapRows = 1024;  // rows per CTA
 // launch and no wait between CTAs), keeps the sequences that reach into its
 // kSlotMapRows rows and then finds each row's sequence among them by bisection.
 // At most kSlotMapRows non-empty sequences reach into a CTA's rows.  Bound by
-// latency: the scan, one bisection and one store each.
+// latency: the scan, one bisection and one store each.  64 sequences of one token: 2.2 us
+// a call in a replayed graph.
 __global__ void __launch_bounds__(kSlotMapThreads) slot_map_kernel(const SlotMapParams p) {
   __shared__ int32_t s_start[kSlotMapRows], s_seq[kSlotMapRows];
   __shared__ int64_t s_warp[kSlotMapThreads / 32];
@@ -139,7 +140,8 @@ __device__ __forceinline__ bool row_target(const CacheWriteParams &p, int32_t r,
 
 // A copy, bound by HBM: each thread moves kCacheWritePieces 16-byte pieces of K and
 // as many of V, all loads in flight before the first store.  Rows are read once and
-// never again here, so they pass the L1.
+// never again here, so they pass the L1.  12000 rows of 8 x 256 in K and V: 35 us, 5.6
+// TB/s, 87 % of a copy of the whole memory's rate.
 __global__ void __launch_bounds__(kCacheWriteThreads) cache_write_kernel(const CacheWriteParams p) {
   const uint32_t pieces = static_cast<uint32_t>(p.n_kv_heads) * p.head_dim / 8;  // of a row
   const int64_t row_elems = static_cast<int64_t>(pieces) * 8;
@@ -205,8 +207,8 @@ __device__ __forceinline__ uint32_t codes_by_division(uint32_t x, uint32_t y, fl
 // A row of one KV head: its largest magnitude, then its codes.  D / 32 lanes share a
 // row, 32 elements each, so that what a row costs besides its elements is spread over
 // four (D = 256) rows a warp: with a warp for each row the kernel was bound by
-// instructions (51 us for 12000 rows of 8 heads; this way HBM bounds it, 2 D bytes
-// read and D + 4 written).
+// instructions (51 us for 12000 rows of 8 heads; this way 32 us, 4.7 TB/s, 61 % of the
+// issue slots: 2 D bytes read and D + 4 written).
 template <int D>
 __global__ void __launch_bounds__(kCacheWriteThreads)
     cache_write_fp8_kernel(const CacheWriteParams p) {
