@@ -35,8 +35,10 @@
 // TMEM: O (256 columns) and four buffers of 64 columns, each first a tile's scores,
 // then, written in place by 16 columns, its weights.
 //
-// Warps: 0 loads tiles, 3 loads Q, 1 issues Q.K and owns TMEM, 2 issues P.V, 4-7
-// and 8-11 run the softmax of even and of odd tiles.  Every wait is bounded.
+// Warps: 3 loads tiles, 0 loads Q, 1 issues Q.K and owns TMEM, 2 issues P.V, 4-7 and
+// 8-11 run the softmax of even and of odd tiles.  (Warps 0, 4 and 8 share a scheduler:
+// where a block has few rows, 4 and 8 have them all, and the tile loader beside them cost
+// a verify step 2 to 3 percent.)  Every wait is bounded.
 //
 // What bounds it: a tile's softmax is a chain of some 4500 cycles (two reads of the
 // scores from tensor memory, the exponentials, the stores of the weights), the same for
@@ -44,7 +46,7 @@
 // take 16 columns and stay rolled, because all of the L1 is in use as shared memory and a
 // spilled register costs a trip to the L2: 32 or 64 columns at a time, or the next read in
 // flight, spill 100 to 560 bytes and take 10 to 25 % longer.  Measured: 64 sequences of 4
-// tokens over windows of 1024 in 133 us (4.1 TB/s), an 8192-token prompt in 238 us (540
+// tokens over windows of 1024 in 130 us (4.2 TB/s), an 8192-token prompt in 238 us (540
 // TFLOP/s of the formula's products, half as many again with the weights' second part), 64
 // sequences behind 8192 shared tokens at head_dim 512 in 75 us.
 //
@@ -56,7 +58,7 @@
 // oempty: a group arrives behind the segment's last P.V, whose first one waited for
 // the phase before.
 //
-// Warp 0 finds the segments and passes them on in eight slots, without waiting for
+// Warp 3 finds the segments and passes them on in eight slots, without waiting for
 // their readers: it writes segment n + 8 in front of loading that segment's first tile
 // i, and to load tile i - 1 it waited for the products of tile i - 6 (or a later one).
 // Tiles i - 7 and i - 6 come behind segment n's first tile, so both softmax groups,
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
   RowsPlan *plan_smem = reinterpret_cast<RowsPlan *>(bars + 66);
   static_assert(sizeof(RowsPlan) <= 9 * 8, "the plan's place");
   volatile int *last_piece = reinterpret_cast<volatile int *>(bars + 75);  // [2 groups]
-  uint64_t *seg_full = bars + 76;  // [8] warp 0 -> everyone: segment n & 7 is there
+  uint64_t *seg_full = bars + 76;  // [8] warp 3 -> everyone: segment n & 7 is there
   constexpr uint32_t kSlots = 8;
   int32_t *seg_slots = reinterpret_cast<int32_t *>(bars + 84);  // [8][kSegmentWords]
   static_assert(84 * 8 + kSlots * kSegmentWords * 4 <= 1024, "barriers and segments");
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
     return any;
   };
 
-  if (warp == 0) {
+  if (warp == 3) {
     // --------------------------------------------------------- tile loads
     // Tiles of a sequence's cache without any of the step's own rows hold what earlier
     // steps wrote and are loaded before the kernel in front has ended.  A prefix may be
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
       if (!(p.test_withhold && f == 0)) mbar_wait(&kfull[f & 7], (f >> 3) & 1, &no_abort, p.status);
     for (uint32_t f = nv > NST ? nv - NST : 0; f < nv; ++f)
       mbar_wait(&vfull[f & 7], (f >> 3) & 1, &no_abort, p.status);
-  } else if (warp == 3) {
+  } else if (warp == 0) {
     // ------------------------------------------------------------ Q loads
     grid_dependency_wait();
     bool has = take(0);
