@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
 #pragma unroll 1
               for (int ch = 0; ch < TILE / CW; ++ch) {
                 float s[CW];
-                tmem_load(s_col + CW * ch, s);
+                tmem_ld16(s_col + CW * ch, s);
 #pragma unroll
                 for (int c = 0; c < CW / 4; ++c)
                   st_peer_v4(dst + (CW / 4 * ch + c) * (Cfg::M * 16), s[4 * c], s[4 * c + 1],
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
 #pragma unroll 1
             for (int ch = 0; ch < TILE / CW; ++ch) {
               float s[CW];
-              if (ok) tmem_load(s_col + CW * ch, s);
+              if (ok) tmem_ld16(s_col + CW * ch, s);
               f(ch, s);
             }
           };
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
                 s[4 * c + 2] += o.z;
                 s[4 * c + 3] += o.w;
               }
-              tmem_store(s_col + CW * ch, s);
+              tmem_store16(s_col + CW * ch, s);
             }
             float m4[4] = {best, best, best, best};
             if (masked) {
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
               w[j + 8] = __uint_as_float(                           // 8 of remainders
                   __byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632));
             }
-            if (ok) tmem_store(s_col + CW * ch, w);
+            if (ok) tmem_store16(s_col + CW * ch, w);
           };
           walk(weigh);
           if (ok) tmem_store_wait();
