@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           }
           // The largest product (times the scale's sign: scale and soft-cap are monotonic).
           float best = -INFINITY;
-          float widest = 0.f;  // with a soft-cap: the largest magnitude, of any column
+          float widest = 0.f;  // with a soft-cap: the largest magnitude among the seen columns
           auto scan = [&](int ch, float (&s)[CW]) {
             if (NH == 2 && ok) {
               const float4 *x = xs + wg * (Cfg::XB / 16) + ch * (CW / 4) * Cfg::M + r;
@@ -663,6 +663,11 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
 #pragma unroll
               for (int c = 0; c < CW; ++c)
                 m4[c & 3] = fmaxf(m4[c & 3], (bits >> c) & 1 ? s[c] * sign : -INFINITY);
+              // A column that nobody sees may hold anything (what shared memory held before,
+              // for one), so it has no say in how the others' weights are computed.
+              if (CAP)
+#pragma unroll
+                for (int c = 0; c < CW; ++c) s[c] = (bits >> c) & 1 ? s[c] : 0.f;
             } else if (sign > 0.f) {
 #pragma unroll
               for (int c = 0; c < CW; c += 2)

@@ -1,0 +1,65 @@
+"""Continuous-batching calls that the header allows and ordinary use rarely makes."""
+import pytest
+import torch
+
+import serving_ref as ref
+from gpu_helpers import require_gpu
+from test_gpu_serving import GLOBAL, SLIDING, Call
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+# ------------------------------------------------------------- the same bits
+CAPPED = {  # tiles that end inside a box of rows, in slots that no token attends
+    "decode": dict(T=1, lens=[70, 3, 130], window=100, sinks=4, **SLIDING),
+    "verify": dict(T=4, lens=[900, 333, 5], window=500, sinks=4, **SLIDING),
+    "chunk": dict(T=70, lens=[200, 75], window=100, sinks=4, capacity=190, **SLIDING),
+    "wide": dict(T=2, lens=[300, 20], window=100, sinks=4, hq=16, hkv=1, dim=512, shared=True),
+    "wide_separate": dict(T=5, lens=[300, 20], window=100, sinks=4, hq=16, hkv=2, dim=512),
+    "prefix": dict(T=1, lens=[5, 90], prefix=101, prefix_rows=257, **GLOBAL),
+    "prefix_window": dict(T=2, lens=[40, 3], prefix=75, prefix_rows=100, window=50, **SLIDING),
+}
+
+
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+@pytest.mark.parametrize("name", list(CAPPED))
+def test_slots_that_nobody_attends_have_no_say(name, softcap):
+    """Whatever stands in them, the result is the same, bit for bit."""
+    want = None
+    for fill in (0.0, 3e4, -3e4, float("nan")):
+        c = ref.make_case(len(name), softcap=softcap, **CAPPED[name])
+        for t in (c.k, c.v, c.pk, c.pv):
+            if t is not None:
+                t.masked_fill_(t.isnan(), fill)
+        got = [t.clone() for t in Call(c).run()]
+        if want is None:
+            ref.check(*got, ref.reference(c, "cuda"))
+            want = got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), fill
+
+
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+@pytest.mark.parametrize("name", list(CAPPED))
+def test_what_ran_before_has_no_say(name, softcap):
+    """Nor has what other calls left on the chip: rows of other sizes between the calls."""
+    call = Call(ref.make_case(len(name), softcap=softcap, **CAPPED[name]))
+    wide = call.desc.head_dim == 512
+    others = []
+    for size in (0.01, 300.0):
+        c = ref.make_case(1, T=1, lens=[2000] * (8 if wide else 2), window=1900, sinks=4,
+                          hq=16, hkv=1 if wide else 8, dim=512 if wide else 256, shared=wide)
+        for t in (c.k, c.v):
+            if t is not None:
+                t *= size
+        others.append(Call(c))
+    want = None
+    for i in range(12):
+        others[i % 2].enqueue()
+        got = [t.clone() for t in call.run()]
+        want = want or got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
