@@ -104,7 +104,9 @@ static_assert(RowsConfig<1>::SMEM <= 227 * 1024 && RowsConfig<2>::SMEM <= 227 * 
 struct RowsParams {
   RowsGeom g;
   uint16_t *out;       // bf16 [T][B][Hq][D]
+  int32_t out_halves;  // out is on a 16-byte boundary only
   float *lse;          // [T][B][Hq] or null
+  // (own_o and pre_o are on 32-byte boundaries)
   float *own_o, *own_lse;  // partials of own units, rs rows a slot; a CTA pair's two have
   int64_t lse_stride;      // a copy of own_lse each, lse_stride elements apart
   float *pre_o, *pre_lse;  // partials of prefix units, rp rows a slot
@@ -881,6 +883,7 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
           }
         } else {
           const int units = final_rows ? DH / 64 : DH / 32;  // 128-byte lines of a row
+          const bool halves = final_rows && p.out_halves != 0;
 #pragma unroll 1
           for (int u = 0; u < units; ++u) {
             uint32_t v[32];
@@ -908,6 +911,13 @@ __global__ void __launch_bounds__(RowsConfig<NH>::kThreads, 1)
               if (lane == 0) mbar_arrive(oempty);
             }
             swap_pieces(v, lane);
+            if (halves) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if ((row_there >> k) & 1)
+                  st_global_2v4(row_base[k] + u * 128 + (lane & 3) * 32, v + 8 * k);
+              continue;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if ((row_there >> k) & 1)

@@ -65,11 +65,18 @@ __device__ __forceinline__ void tmem_store_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 32 bytes to global memory (32-byte aligned): one sector per lane.
+// 32 bytes to global memory: one sector per lane.
+// On a 32-byte boundary ...
 __device__ __forceinline__ void st_global_v8(void *dst, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+// ... and on a 16-byte one.
+__device__ __forceinline__ void st_global_2v4(void *dst, const uint32_t *v) {
+  uint4 *to = static_cast<uint4 *>(dst);
+  to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+  to[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
 // Four neighbouring lanes with four pieces of 8 words each: afterwards lane j holds,

@@ -192,7 +192,9 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
   lay.pre_lse = align256(lay.own_lse + lay.nh * own_rows * 4);
   lay.own_o = align256(lay.pre_lse + pre_rows * 4);
   lay.pre_o = align256(lay.own_o + own_rows * d->head_dim * 4);
-  lay.bytes = align256(lay.pre_o + pre_rows * d->head_dim * 4);
+  // The row kernel stores 32 bytes at a time, and a workspace may start between two
+  // 32-byte boundaries: room to move own_o and pre_o up to the next.
+  lay.bytes = align256(lay.pre_o + pre_rows * d->head_dim * 4 + 16);
   return GDATTN_OK;
 }
 
@@ -250,11 +252,13 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
   RowsParams p = {};
   p.g = g;
   p.out = static_cast<uint16_t *>(out);
+  p.out_halves = (reinterpret_cast<uintptr_t>(out) & 31u) != 0 ? 1 : 0;
   p.lse = lse;
-  p.own_o = reinterpret_cast<float *>(ws + lay.own_o);
+  const size_t up = (0 - reinterpret_cast<uintptr_t>(ws)) & 31u;  // 0 or 16
+  p.own_o = reinterpret_cast<float *>(ws + lay.own_o + up);
   p.own_lse = reinterpret_cast<float *>(ws + lay.own_lse);
   p.lse_stride = lay.lse_stride;
-  p.pre_o = reinterpret_cast<float *>(ws + lay.pre_o);
+  p.pre_o = reinterpret_cast<float *>(ws + lay.pre_o + up);
   p.pre_lse = reinterpret_cast<float *>(ws + lay.pre_lse);
   // A block of few rows is joined by the row kernel itself; with more rows the four warps
   // that would do it take longer than a kernel with a warp for each.

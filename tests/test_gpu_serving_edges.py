@@ -3,7 +3,8 @@ import pytest
 import torch
 
 import serving_ref as ref
-from gpu_helpers import require_gpu
+from decode_attention_09_b200 import binding
+from gpu_helpers import GUARD_BYTE, GUARD_BYTES, require_gpu
 from test_gpu_serving import GLOBAL, SLIDING, Call
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +64,55 @@ def test_what_ran_before_has_no_say(name, softcap):
         got = [t.clone() for t in call.run()]
         want = want or got
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
+
+
+# ---------------------------------------------------------------- alignment
+class AtHalf:
+    """A device tensor that starts at an odd multiple of 16 bytes, between guard bytes."""
+
+    def __init__(self, like):
+        n = like.numel() * like.element_size()
+        self.lo, self.hi = GUARD_BYTES + 16, GUARD_BYTES + 16 + n
+        self.raw = torch.full((self.hi + GUARD_BYTES,), GUARD_BYTE, dtype=torch.uint8,
+                              device="cuda")
+        self.t = self.raw[self.lo:self.hi].view(like.dtype).view(like.shape)
+        assert self.t.data_ptr() % 32 == 16
+
+    def check(self, what):
+        assert (self.raw[:self.lo] == GUARD_BYTE).all(), f"{what}: written in front"
+        assert (self.raw[self.hi:] == GUARD_BYTE).all(), f"{what}: written behind"
+
+
+HALF = {  # what a block writes, by its rows and how its unit is cut
+    "whole_units": dict(T=1, lens=[300, 70], window=200, sinks=4, **SLIDING),
+    "whole_blocks": dict(T=130, lens=[300], window=100, sinks=4, **SLIDING),
+    "few_rows": dict(T=1, lens=[900, 70], window=700, sinks=4, **SLIDING),
+    "some_rows": dict(T=4, lens=[900, 333], window=500, sinks=4, softcap=50.0, **SLIDING),
+    "full_blocks": dict(T=70, lens=[900], window=700, sinks=4, **SLIDING),
+    "wide_few_rows": dict(T=1, lens=[900], window=700, sinks=4, hq=4, hkv=1, dim=512),
+    "wide_some_rows": dict(T=1, lens=[900, 20, 0], window=700, sinks=4, hq=16, hkv=1, dim=512,
+                           shared=True),
+    "wide_full_blocks": dict(T=20, lens=[900], window=700, sinks=4, hq=16, hkv=1, dim=512,
+                             shared=True, softcap=30.0),
+    "prefix": dict(T=1, lens=[40, 3], prefix=100, window=0, **SLIDING),
+    "wide_prefix": dict(T=2, lens=[40, 3, 300], prefix=333, **GLOBAL),
+}
+
+
+@pytest.mark.parametrize("split", [1, 0])
+@pytest.mark.parametrize("name", list(HALF))
+def test_outputs_and_workspace_on_a_16_byte_boundary(name, split):
+    """16 bytes are all that a pointer has to be aligned to: the result is the same, bit
+    for bit, as on wider boundaries."""
+    c = ref.make_case(seed=len(name), **HALF[name])
+    call = Call(c, split)
+    want = [t.clone() for t in call.run()]
+    ref.check(*want, ref.reference(c, "cuda"))
+    for moved in (("out",), ("ws",), ("out", "ws")):
+        call = Call(c, split)
+        for n in moved:
+            setattr(call, n, AtHalf(getattr(call, n).t))
+        binding.workspace_init(call.ws.t)
+        call.out.t.fill_(float("nan"))
+        got = call.run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), moved
