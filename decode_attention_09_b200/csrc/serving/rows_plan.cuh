@@ -51,8 +51,9 @@ struct RowRange {
 
 GDATTN_HD RowRange own_row_range(const RowsGeom &g, int32_t L, int32_t t) {
   RowRange r = {0, 0, 0};
+  if (L <= 0) return r;  // a padding entry
   const int32_t p = L - g.tokens + t;
-  if (L <= 0 || p < 0) return r;  // a padding entry, or a token in front of the sequence
+  if (p < 0) return r;  // a token in front of the sequence
   r.hi = p + 1;
   r.lo = g.window > 0 ? imax32(0, p + 1 - g.window) : 0;
   r.pin = g.sinks;
@@ -61,8 +62,9 @@ GDATTN_HD RowRange own_row_range(const RowsGeom &g, int32_t L, int32_t t) {
 
 GDATTN_HD RowRange prefix_row_range(const RowsGeom &g, int32_t L, int32_t t, int32_t P) {
   RowRange r = {0, 0, 0};
+  if (L <= 0) return r;
   const int32_t p = L - g.tokens + t;
-  if (L <= 0 || p < 0) return r;
+  if (p < 0) return r;
   r.hi = P;
   const int64_t lo = g.window > 0 ? static_cast<int64_t>(P) + p + 1 - g.window : 0;
   r.lo = lo <= 0 ? 0 : (lo < P ? static_cast<int32_t>(lo) : P);
@@ -130,10 +132,13 @@ GDATTN_HD RowTile unit_tile(const UnitTiles &u, int32_t t) {
 GDATTN_HD UnitTiles own_unit(const RowsGeom &g, int32_t L, int32_t qb, bool &bad) {
   UnitTiles u = {0, 0, 0, 0, 0, g.sinks, 0, 0, 1};
   if (bad_length(g, L)) bad = true;
+  if (L <= 0) return u;
   const int32_t first = L - g.tokens + qb * g.qt_seq;
   const int32_t hi = first + imin32(g.qt_seq, g.tokens - qb * g.qt_seq);
-  if (L <= 0 || hi <= 0) return u;
-  int32_t lo = g.window > 0 ? imax32(0, first + 1 - g.window) : 0;
+  if (hi <= 0) return u;
+  // (compared first: with a window near 2^31 and a sequence shorter than the step the
+  // difference leaves 32 bits)
+  int32_t lo = g.window > 0 && first + 1 > g.window ? first + 1 - g.window : 0;
   const int32_t oldest = oldest_in_ring(g, L);
   if (imax32(lo, g.sinks) < oldest) {  // positions that later ones overwrote
     bad = true;

@@ -116,3 +116,20 @@ def test_outputs_and_workspace_on_a_16_byte_boundary(name, split):
         call.out.t.fill_(float("nan"))
         got = call.run()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), moved
+
+
+# ------------------------------------------------------------ the ends of 32 bits
+@pytest.mark.parametrize("dim,hkv,shared", [(256, 8, False), (512, 1, True)])
+@pytest.mark.parametrize("sinks", [0, 3])
+@pytest.mark.parametrize("split", [0, 5])
+def test_the_widest_window(dim, hkv, shared, sinks, split):
+    """A window of 2^31 - 1 (everything is visible), also over sequences shorter than
+    the step, whose tokens in front of position 0 get 0."""
+    kw = dict(hq=16, hkv=hkv, dim=dim, window=2 ** 31 - 1, sinks=sinks, shared=shared)
+    for T, lens, status in ((9, [4, 30, 0, 8], binding.GDATTN_ERR_DEVICE_SEQLEN),
+                            (70, [3, 200], binding.GDATTN_ERR_DEVICE_SEQLEN),
+                            (1, [1, 300, 64], binding.GDATTN_OK),
+                            (66, [66, 130], binding.GDATTN_OK)):
+        c = ref.make_case(T, T, lens, **kw)
+        out, lse = Call(c, split).run(status)
+        ref.check(out, lse, ref.reference(c, "cuda"))
