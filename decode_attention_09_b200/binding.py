@@ -142,6 +142,29 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for a call on ``stream`` (None: the current one).  The caching allocator
+    hands memory out again in the order of the stream it was allocated on, so what a
+    wrapper allocates belongs to the stream its kernels run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)  # 0 and 1 are the legacy default stream
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1) else
+                  torch.cuda.ExternalStream(handle, device=device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on ``stream``, which the current stream may read after the
+    caller has ordered the two: its memory is not used again before that read."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dense(t: torch.Tensor, name: str, dtypes, numel: int, device) -> None:
     """A dense tensor argument: one of ``dtypes``, contiguous, holding at least
     ``numel`` elements (what the call reads or writes through its pointer), on
@@ -293,7 +316,7 @@ def alloc_workspace(batch: int, max_seqlen: int, desc: LayerDesc, device="cuda",
     n = workspace_size(batch, max_seqlen, desc)
     if n == 0:
         raise GdattnError(GDATTN_ERR_INVALID_ARG, "gdattn_workspace_size")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = _empty((n,), torch.uint8, device, stream)
     workspace_init(ws, stream)
     return ws
 
@@ -313,9 +336,9 @@ def decode(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], seqlens:
     """One decode-attention layer through gdattn_decode.  Returns (out, lse)."""
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _result((B, Hq, D), torch.bfloat16, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _result((B, Hq), torch.float32, q.device, stream)
     _check_layer(q, k, v, seqlens, out, lse, desc, B, B)
     if workspace is None:
         workspace = alloc_workspace(B, max_seqlen, desc, q.device, stream)
@@ -336,9 +359,9 @@ def decode_append(q: torch.Tensor, k_new: torch.Tensor, v_new: Optional[torch.Te
     (L - 1) mod C of the caches, then decode.  Returns (out, lse)."""
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _result((B, Hq, D), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _result((B, Hq), torch.float32, q.device, stream)
     _check_layer(q, k, v, seqlens, out, lse, desc, B, B)
     _check_new_rows(k_new, v_new, desc, B, q.device)
     if workspace is None:
@@ -373,9 +396,9 @@ def decode_fp8(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
     """
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _result((B, Hq, D), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _result((B, Hq), torch.float32, q.device, stream)
     _check_fp8(q, k_codes, v_codes, k_scale, v_scale, seqlens, out, lse, desc, B)
     if workspace is None:
         workspace = alloc_workspace(B, max_seqlen, desc, q.device, stream)
@@ -410,15 +433,15 @@ def decode_multi(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
     L_b - T + t, attending causally.  Returns (out, lse), token-major."""
     T, B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((T, B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _result((T, B, Hq, D), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, B, Hq), dtype=torch.float32, device=q.device)
+        lse = _result((T, B, Hq), torch.float32, q.device, stream)
     _check_layer(q, k, v, seqlens, out, lse, desc, T * B, B)
     if workspace is None:
         n = multi_workspace_size(B, T, max_seqlen, desc)
         if n == 0:
             raise GdattnError(GDATTN_ERR_INVALID_ARG, "gdattn_multi_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _empty((n,), torch.uint8, q.device, stream)
         workspace_init(workspace, stream)
     _on(workspace, "workspace", q.device)
     st = decode_multi_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(seqlens), B, T, max_seqlen, desc,
@@ -460,9 +483,9 @@ def combine(o_partial: torch.Tensor, lse_partial: torch.Tensor, out: Optional[to
     """gdattn_combine: o_partial fp32 [B,Hq,S,D], lse_partial fp32 [B,Hq,S]."""
     B, Hq, S, D = o_partial.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=o_partial.device)
+        out = _result((B, Hq, D), torch.bfloat16, o_partial.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=o_partial.device)
+        lse = _result((B, Hq), torch.float32, o_partial.device, stream)
     _check_combine(o_partial, lse_partial, out, lse)
     st = lib().gdattn_combine(_ptr(o_partial), _ptr(lse_partial), B, Hq, S, D, _ptr(out), _ptr(lse),
                               _stream_handle(stream))
@@ -527,10 +550,11 @@ def _need_cache(t: torch.Tensor, name: str, dtypes, numel: int, like: torch.Tens
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _check_tokens(q, k, v, seqlens, out, lse, desc):
+def _check_tokens(q, k, v, seqlens, out, lse, desc, stream=None):
     """The arguments both continuous-batching attention calls share: q and out bf16
     [T, B, Hq, D], lse fp32 [T, B, Hq] or None, caches spanning B sequences.  Returns
-    (T, B, device index, out, lse), with out and lse allocated where they are None."""
+    (T, B, device index, out, lse), with out and lse allocated where they are None, for
+    a call on ``stream``."""
     T, B, Hq, D = q.shape
     index = q.get_device()
     if Hq != desc.n_q_heads or D != desc.head_dim:
@@ -539,11 +563,13 @@ def _check_tokens(q, k, v, seqlens, out, lse, desc):
     if index < 0 or q.dtype is not _bf16 or not q.is_contiguous():
         _dense(q, "q", _BF16, q.numel(), q.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = (torch.empty_like(q) if stream is None else
+               _result(q.shape, _bf16, q.device, stream))
     else:
         _need(out, "out", _bf16, T * B * Hq * D, q, index)
     if lse is None:
-        lse = q.new_empty((T, B, Hq), dtype=_f32)
+        lse = (q.new_empty((T, B, Hq), dtype=_f32) if stream is None else
+               _result((T, B, Hq), _f32, q.device, stream))
     else:
         _need(lse, "lse", _f32, T * B * Hq, q, index)
     n = _cache_elems(B, desc)
@@ -592,7 +618,7 @@ def _zeroed_workspace(size, what: str, device, stream) -> torch.Tensor:
         n = size()
         if n == 0:
             raise GdattnError(GDATTN_ERR_INVALID_ARG, what)
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws = _empty((n,), torch.uint8, device, stream)
         workspace_init(ws, stream)
     return ws
 
@@ -612,7 +638,7 @@ def decode_sink(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
     """Sliding-window attention with n_sink pinned first tokens through
     gdattn_decode_sink.  q bf16 [T, B, Hq, D]: token t of sequence b at position
     L_b - T + t.  Returns (out, lse), token-major."""
-    T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
+    T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc, stream)
     if workspace is None:
         workspace = alloc_sink_workspace(B, T, max_seqlen, desc, n_sink, q.device, stream)
     _check_workspace(workspace, q, index)
@@ -642,7 +668,7 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: Optional[to
     q bf16 [T, B, Hq, D]; k_prefix / v_prefix bf16 [prefix_rows, Hkv, D] (v_prefix None
     when K = V); prefix_len int32 [1] on the device; k, v, seqlens the sequences' own
     caches and lengths.  Returns (out, lse), token-major."""
-    T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc)
+    T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc, stream)
     rows = k_prefix.shape[0]
     n = rows * desc.n_kv_heads * desc.head_dim
     _need(k_prefix, "k_prefix", _bf16, n, q, index)
@@ -680,7 +706,9 @@ def slot_map(seqlens: torch.Tensor, new_lens: torch.Tensor, n_rows: int, capacit
     if n_rows < 0:
         raise ValueError(f"n_rows: {n_rows}")
     if out is None:
-        flat = seqlens.new_empty(B + 1 + 3 * n_rows)
+        n = B + 1 + 3 * n_rows
+        flat = (seqlens.new_empty(n) if stream is None else
+                _result((n,), _i32, seqlens.device, stream))
         out = RowMap(*flat.split_with_sizes((B + 1, n_rows, n_rows, n_rows)))
         start = flat.data_ptr()
         seq = start + 4 * (B + 1)
