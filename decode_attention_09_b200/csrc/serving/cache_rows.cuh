@@ -178,9 +178,11 @@ __global__ void __launch_bounds__(kCacheWriteThreads) cache_write_kernel(const C
 // within 2^-47 of the quotient before its one rounding.  That rounding could only go
 // the other way next to a midpoint of fp32, which a bf16 x over a scale that is itself
 // x' / 448 never comes that close to; the tests go through every pair of mantissas.
+// (The remainder is taken as q s - x and its product subtracted, so that a zero keeps
+// its sign: x - q s is +0 for x = -0.)
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
+  return fmaf(fmaf(q, s, -x), -r, q);
 }
 
 // Scales that leave the reciprocal, the guess and its remainder (2^-46 of the product)

@@ -133,3 +133,28 @@ def test_the_widest_window(dim, hkv, shared, sinks, split):
         c = ref.make_case(T, T, lens, **kw)
         out, lse = Call(c, split).run(status)
         ref.check(out, lse, ref.reference(c, "cuda"))
+
+
+# ------------------------------------------------------------------ fp8 codes
+@pytest.mark.parametrize("dim", [256, 512])
+def test_fp8_codes_byte_by_byte(dim):
+    """Codes as bytes: a zero has its sign, whichever way the scale makes the kernel
+    divide, and so has what rounds to zero; a row of zeros has codes and scale 0."""
+    g = torch.Generator().manual_seed(dim)
+    x = torch.randn((60, 1, dim), generator=g).to(torch.bfloat16)
+    x[:, :, ::7], x[:, :, 1::7] = -0.0, 0.0
+    x[:, :, 2::7] *= 2.0 ** -14  # below half of e4m3's smallest number
+    x *= torch.exp2(torch.arange(-120.0, 120.0, 4.0))[:, None, None].to(torch.bfloat16)
+    x[5], x[6] = 0.0, -0.0
+    n = x.shape[0]
+    desc = binding.make_desc(1, 1, dim, 0, 0.0, 1.0, True, n)
+    codes = torch.full((1, n, 1, dim), 0x55, dtype=torch.uint8, device="cuda")
+    scale = torch.full((1, 1, n), -1.0, device="cuda")
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    binding.cache_write_fp8(x.cuda(), None, torch.zeros_like(at), at, desc, codes, None, scale)
+    s = x.float().abs().amax(-1) / 448
+    want = (x.float() / s[..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    want[s[:, 0] == 0] = 0
+    assert (want == 0x80).sum() > 60 * dim // 7 - 200  # the signs are there to be lost
+    assert torch.equal(scale.cpu().view(-1), s.view(-1))
+    assert torch.equal(codes.cpu().view(n, 1, dim), want)
