@@ -118,20 +118,28 @@ int blocks_per_sm(F fn, int threads, int smem) {
 
 struct KernelInfo {
   const void *key;
+  unsigned long long ctx_id;  // the context whose limits were set
   int blocks;
 };
 
-// Resident blocks per SM for each kernel instantiation, measured once.
+// Resident blocks per SM for each kernel instantiation, measured once in a context: the
+// shared-memory limit that the query sets belongs to it too.
 int cached_blocks_per_sm(const void *key, int threads, int smem,
                          int (*query)(const void *, int, int)) {
   static std::mutex mu;
   static KernelInfo cache[64];
   static int used = 0;
+  const unsigned long long ctx_id = current_context_id();
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used; ++i)
-    if (cache[i].key == key) return cache[i].blocks;
+  int at = 0;
+  while (at < used && cache[at].key != key) ++at;
+  if (at < used && ctx_id != 0 && cache[at].ctx_id == ctx_id) return cache[at].blocks;
   const int nb = query(key, threads, smem);
-  if (nb > 0 && used < 64) cache[used++] = KernelInfo{key, nb};
+  // (without a current context the query has made one)
+  if (nb > 0 && at < 64) {
+    cache[at] = KernelInfo{key, ctx_id != 0 ? ctx_id : current_context_id(), nb};
+    if (at == used) ++used;
+  }
   return nb;
 }
 
@@ -799,36 +807,6 @@ size_t multi_bytes(const LayerPlan &pl, int32_t batch, int32_t T) {
 
 // -------------------------------------------------- fixed scratch (no alloc)
 constexpr int kMaxDevices = 64;
-
-// Process-unique id of the current CUDA context (cuCtxGetId), so that a
-// context created after a reset is never mistaken for its predecessor even if
-// it reuses the handle.  0 when the driver cannot say.
-unsigned long long current_context_id() {
-  using CtxGetCurrentFn = CUresult (*)(CUcontext *);
-  using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
-  static CtxGetCurrentFn get_current = []() -> CtxGetCurrentFn {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<CtxGetCurrentFn>(p);
-  }();
-  static CtxGetIdFn get_id = []() -> CtxGetIdFn {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<CtxGetIdFn>(p);
-  }();
-  CUcontext ctx = nullptr;
-  unsigned long long id = 0;
-  if (get_current == nullptr || get_id == nullptr || get_current(&ctx) != CUDA_SUCCESS ||
-      ctx == nullptr || get_id(ctx, &id) != CUDA_SUCCESS)
-    return 0;
-  return id;
-}
 
 // Address of g_noalloc_scratch in the current device's context.  The first
 // call in a context looks it up and enqueues a clear of the whole array on

@@ -37,6 +37,36 @@ inline int sm_count() {
   return n;
 }
 
+// Process-unique id of the current CUDA context (cuCtxGetId), so that a
+// context created after a reset is never mistaken for its predecessor even if
+// it reuses the handle.  0 when the driver cannot say.
+inline unsigned long long current_context_id() {
+  using CtxGetCurrentFn = CUresult (*)(CUcontext *);
+  using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
+  static CtxGetCurrentFn get_current = []() -> CtxGetCurrentFn {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<CtxGetCurrentFn>(p);
+  }();
+  static CtxGetIdFn get_id = []() -> CtxGetIdFn {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<CtxGetIdFn>(p);
+  }();
+  CUcontext ctx = nullptr;
+  unsigned long long id = 0;
+  if (get_current == nullptr || get_id == nullptr || get_current(&ctx) != CUDA_SUCCESS ||
+      ctx == nullptr || get_id(ctx, &id) != CUDA_SUCCESS)
+    return 0;
+  return id;
+}
+
 // ----------------------------------------------------------------- checks
 inline gdattn_status check_desc(const gdattn_layer_desc *d) {
   if (d == nullptr) return GDATTN_ERR_INVALID_ARG;

@@ -92,17 +92,23 @@ cudaLaunchConfig_t rows_launch(int nh, int workers, cudaStream_t stream,
 }
 
 // CTAs (or CTA pairs) of the geometry's kernel that the current device holds at
-// once; also sets the kernel's shared-memory limit there.  Found once per device.
+// once; also sets the kernel's shared-memory limit.  Found once per context: the limit
+// belongs to it.
 int max_workers(const gdattn_layer_desc *d) {
   constexpr int kDevices = 64;
+  struct Entry {
+    unsigned long long ctx_id;
+    int n;
+  };
   static std::mutex mu;
-  static int known[kDevices][2][2][2] = {};
+  static Entry known[kDevices][2][2][2] = {};
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
   const int nh = d->head_dim / 256;
-  int &n = known[dev][nh - 1][d->kv_shared][d->softcap > 0.f ? 1 : 0];
+  Entry &e = known[dev][nh - 1][d->kv_shared][d->softcap > 0.f ? 1 : 0];
+  const unsigned long long ctx_id = current_context_id();  // 0: there is none yet
   std::lock_guard<std::mutex> lock(mu);
-  if (n > 0) return n;
+  if (ctx_id != 0 && e.ctx_id == ctx_id) return e.n;
   const void *fn = reinterpret_cast<const void *>(rows_kernel(d));
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            nh == 1 ? RowsConfig<1>::SMEM : RowsConfig<2>::SMEM) != cudaSuccess)
@@ -125,7 +131,8 @@ int max_workers(const gdattn_layer_desc *d) {
     cudaLaunchConfig_t cfg = rows_launch(nh, sm_count() / 2, nullptr, attr);
     if (cudaOccupancyMaxActiveClusters(&got, fn, &cfg) != cudaSuccess) return 0;
   }
-  return n = got;
+  if (got > 0) e = {ctx_id != 0 ? ctx_id : current_context_id(), got};
+  return got;
 }
 
 struct RowsLayout {
