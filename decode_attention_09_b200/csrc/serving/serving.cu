@@ -92,27 +92,31 @@ cudaLaunchConfig_t rows_launch(int nh, int workers, cudaStream_t stream,
 }
 
 // CTAs (or CTA pairs) of the geometry's kernel that the current device holds at
-// once; also sets the kernel's shared-memory limit.  Found once per context: the limit
-// belongs to it.
-int max_workers(const gdattn_layer_desc *d) {
+// once, and its SMs; also sets the kernel's shared-memory limit.  Found once per context:
+// the limit belongs to it.
+struct DeviceRoom {
+  int workers, sms;
+};
+
+DeviceRoom device_room(const gdattn_layer_desc *d) {
   constexpr int kDevices = 64;
   struct Entry {
     unsigned long long ctx_id;
-    int n;
+    DeviceRoom room;
   };
   static std::mutex mu;
   static Entry known[kDevices][2][2][2] = {};
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return {};
   const int nh = d->head_dim / 256;
   Entry &e = known[dev][nh - 1][d->kv_shared][d->softcap > 0.f ? 1 : 0];
   const unsigned long long ctx_id = current_context_id();  // 0: there is none yet
   std::lock_guard<std::mutex> lock(mu);
-  if (ctx_id != 0 && e.ctx_id == ctx_id) return e.n;
+  if (ctx_id != 0 && e.ctx_id == ctx_id) return e.room;
   const void *fn = reinterpret_cast<const void *>(rows_kernel(d));
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            nh == 1 ? RowsConfig<1>::SMEM : RowsConfig<2>::SMEM) != cudaSuccess)
-    return 0;
+    return {};
   // The merge runs between row kernels: with the same split of L1 and shared memory the
   // SMs need no reconfiguration, which each way waits for an idle SM.
   const void *merges[2] = {nh == 1 ? reinterpret_cast<const void *>(merge_cut_units_kernel<256>)
@@ -122,22 +126,22 @@ int max_workers(const gdattn_layer_desc *d) {
   for (const void *m : merges)
     if (cudaFuncSetAttribute(m, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-      return 0;
-  int got = 0;
+      return {};
+  DeviceRoom got = {0, sm_count()};
   if (nh == 1) {
-    got = sm_count();
+    got.workers = got.sms;
   } else {
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = rows_launch(nh, sm_count() / 2, nullptr, attr);
-    if (cudaOccupancyMaxActiveClusters(&got, fn, &cfg) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = rows_launch(nh, got.sms / 2, nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&got.workers, fn, &cfg) != cudaSuccess) return {};
   }
-  if (got > 0) e = {ctx_id != 0 ? ctx_id : current_context_id(), got};
+  if (got.workers > 0) e = {ctx_id != 0 ? ctx_id : current_context_id(), got};
   return got;
 }
 
 struct RowsLayout {
   RowsGeom g = {};
-  int nh = 1, workers = 0;
+  int nh = 1, workers = 0, sms = 0;
   int32_t rs = 0, rp = 0;
   int64_t lse_stride = 0;
   size_t table = 0, own_o = 0, own_lse = 0, pre_o = 0, pre_lse = 0, bytes = 0;
@@ -179,8 +183,10 @@ gdattn_status plan_layout(int32_t batch, int32_t n_tokens, const gdattn_layer_de
                              (prefix_rows / kRowTile + 1 + g.unit_cost)
                        : 0);
   if (most_steps > INT32_MAX) return GDATTN_ERR_UNSUPPORTED;
-  const int most = max_workers(d);
+  const DeviceRoom room = device_room(d);
+  const int most = room.workers;
   if (most <= 0) return GDATTN_ERR_CUDA;
+  lay.sms = room.sms;
   lay.nh = d->head_dim / 256;
   lay.workers = d->split_ctas > 0 && d->split_ctas < most ? d->split_ctas : most;
   const int64_t own_slots = prefix_rows > 0 ? lay.workers + own_units : 2 * lay.workers;
@@ -292,7 +298,8 @@ gdattn_status enqueue_rows(RowsLayout &lay, const void *q, const void *k_prefix,
                                  ? static_cast<int64_t>(g.batch) * g.tokens * Hq
                                  : static_cast<int64_t>(lay.workers) * lay.rs;
   p.merge_shares = 1;
-  while (p.merge_shares < kMergeWarps && merge_rows * p.merge_shares < 148 * 2 * kMergeWarps)
+  while (p.merge_shares < kMergeWarps &&
+         merge_rows * p.merge_shares < static_cast<int64_t>(lay.sms) * 2 * kMergeWarps)
     p.merge_shares *= 2;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = rows_launch(lay.nh, lay.workers, stream, attr);
