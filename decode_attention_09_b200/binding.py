@@ -669,7 +669,11 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: Optional[to
     when K = V); prefix_len int32 [1] on the device; k, v, seqlens the sequences' own
     caches and lengths.  Returns (out, lse), token-major."""
     T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc, stream)
-    rows = k_prefix.shape[0]
+    shape = k_prefix.shape
+    rows = shape[0]
+    if len(shape) != 3 or shape[1] != desc.n_kv_heads or shape[2] != desc.head_dim:
+        raise ValueError(f"k_prefix: shape {tuple(shape)}, expected "
+                         f"{('prefix_rows', int(desc.n_kv_heads), int(desc.head_dim))}")
     n = rows * desc.n_kv_heads * desc.head_dim
     _need(k_prefix, "k_prefix", _bf16, n, q, index)
     if v_prefix is not None:

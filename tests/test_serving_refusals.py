@@ -1,0 +1,45 @@
+"""Arguments of the continuous-batching wrappers that the C ABI cannot see, or would see
+cut down to 32 bits, on the CPU."""
+import pytest
+import torch
+
+from decode_attention_09_b200 import binding
+
+H, HKV, D, C, B = 16, 8, 256, 8, 2
+
+
+@pytest.fixture(autouse=True)
+def checks_only(monkeypatch):
+    """CPU tensors stand in for device ones, and no call may get past the checks."""
+    monkeypatch.setattr(binding, "_on", lambda *a: None)
+
+    def call(fn, what, *a):
+        raise AssertionError(f"{what} was called")
+
+    monkeypatch.setattr(binding, "_call", call)
+
+
+def z(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def desc():
+    return binding.make_desc(H, HKV, D, 4, 0.0, 1.0, False, C)
+
+
+ws = z(512, dtype=torch.uint8)
+lens = z(B, dtype=torch.int32)
+
+
+def prefix(k_prefix, max_seqlen=8):
+    binding.decode_prefix(z(1, B, H, D), k_prefix, k_prefix, z(1, dtype=torch.int32),
+                          z(B, C, HKV, D), z(B, C, HKV, D), lens, desc(), max_seqlen,
+                          workspace=ws)
+
+
+@pytest.mark.parametrize("shape", [(1, 5, HKV, D), (5, HKV * D), (5, D, HKV), (HKV, 5, D),
+                                   (5 * HKV, 1, D)])
+def test_a_prefix_of_another_shape(shape):
+    """Read as rows, it would be a shorter prefix or other heads."""
+    with pytest.raises(ValueError, match="k_prefix: shape"):
+        prefix(z(*shape))
