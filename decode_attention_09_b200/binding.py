@@ -580,6 +580,13 @@ def _check_tokens(q, k, v, seqlens, out, lse, desc, stream=None):
     return T, B, index, out, lse
 
 
+_MOST = 2 ** 31 - 1  # of the ABI's counts: ctypes would cut higher bits off silently
+
+
+def _too_many(name: str, n: int) -> None:
+    raise ValueError(f"{name}: {n}, at most {_MOST}")
+
+
 def _check_workspace(workspace, like, index: int) -> None:
     _need(workspace, "workspace", _u8, 0, like, index)
 
@@ -639,6 +646,8 @@ def decode_sink(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor],
     gdattn_decode_sink.  q bf16 [T, B, Hq, D]: token t of sequence b at position
     L_b - T + t.  Returns (out, lse), token-major."""
     T, B, index, out, lse = _check_tokens(q, k, v, seqlens, out, lse, desc, stream)
+    if max_seqlen > _MOST or n_sink > _MOST:
+        _too_many("max_seqlen or n_sink", max(max_seqlen, n_sink))
     if workspace is None:
         workspace = alloc_sink_workspace(B, T, max_seqlen, desc, n_sink, q.device, stream)
     _check_workspace(workspace, q, index)
@@ -674,6 +683,8 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: Optional[to
     if len(shape) != 3 or shape[1] != desc.n_kv_heads or shape[2] != desc.head_dim:
         raise ValueError(f"k_prefix: shape {tuple(shape)}, expected "
                          f"{('prefix_rows', int(desc.n_kv_heads), int(desc.head_dim))}")
+    if max_seqlen > _MOST or rows > _MOST:
+        _too_many("max_seqlen or k_prefix rows", max(max_seqlen, rows))
     n = rows * desc.n_kv_heads * desc.head_dim
     _need(k_prefix, "k_prefix", _bf16, n, q, index)
     if v_prefix is not None:
@@ -709,6 +720,8 @@ def slot_map(seqlens: torch.Tensor, new_lens: torch.Tensor, n_rows: int, capacit
         _on(seqlens, "seqlens", None)
     if n_rows < 0:
         raise ValueError(f"n_rows: {n_rows}")
+    if n_rows > _MOST or capacity > _MOST or n_sink > _MOST:
+        _too_many("n_rows, capacity or n_sink", max(n_rows, capacity, n_sink))
     if out is None:
         n = B + 1 + 3 * n_rows
         flat = (seqlens.new_empty(n) if stream is None else
@@ -748,6 +761,8 @@ def _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, dtypes):
     """The arguments both cache writes share; returns (n_rows, batch, row stride)."""
     index = k.get_device()
     n_rows, batch = row_slot.numel(), k.shape[0]
+    if n_rows > _MOST:
+        _too_many("row_slot", n_rows)
     _need(row_seq, "row_seq", _i32, n_rows, k, index)
     _need(row_slot, "row_slot", _i32, n_rows, k, index)
     stride = _row_stride(k_rows, "k_rows", desc, n_rows, k, index)

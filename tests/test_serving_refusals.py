@@ -43,3 +43,25 @@ def test_a_prefix_of_another_shape(shape):
     """Read as rows, it would be a shorter prefix or other heads."""
     with pytest.raises(ValueError, match="k_prefix: shape"):
         prefix(z(*shape))
+
+
+@pytest.mark.parametrize("wide", [2 ** 31, 2 ** 32 + 8, 2 ** 40])
+def test_counts_beyond_32_bits(wide):
+    with pytest.raises(ValueError, match="at most"):
+        prefix(z(5, HKV, D), wide)
+    for max_seqlen, n_sink in ((wide, 2), (8, wide)):
+        with pytest.raises(ValueError, match="at most"):
+            binding.decode_sink(z(1, B, H, D), z(B, C, HKV, D), z(B, C, HKV, D), lens, desc(),
+                                max_seqlen, n_sink, workspace=ws)
+    for n_rows, capacity, n_sink in ((wide, 8, 0), (4, wide, 0), (4, 8, wide)):
+        with pytest.raises(ValueError, match="at most"):
+            binding.slot_map(lens, lens, n_rows, capacity, n_sink)
+
+
+def test_more_rows_than_32_bits_count():
+    many = torch.zeros(1, dtype=torch.int32).expand(2 ** 31)
+    rows = z(1, HKV, D).expand(2 ** 31, HKV, D)
+    cache = z(B, C, HKV, D)
+    for dtypes in (binding._BF16, binding._CODES):
+        with pytest.raises(ValueError, match="at most"):
+            binding._check_write(rows, rows, many, many, desc(), cache, cache, dtypes)
