@@ -542,9 +542,22 @@ def _need(t: torch.Tensor, name: str, dtype, numel: int, like: torch.Tensor, ind
 
 
 def _need_cache(t: torch.Tensor, name: str, dtypes, numel: int, like: torch.Tensor,
-                index: int) -> None:
+                index: int, desc: LayerDesc) -> None:
     if not _fits(t, dtypes[0], numel, index):  # dense caches; strided ones reach further
         _extent(t, name, dtypes, numel, like.device)
+        if t.dim() == 4 and not t.is_contiguous():
+            _cache_strides(t, name, desc)
+
+
+def _cache_strides(t: torch.Tensor, name: str, desc: LayerDesc) -> None:
+    """A cache [B, C, Hkv, D] that is not contiguous: the library goes by the descriptor,
+    so any other order or distance of the rows would be read as something else."""
+    H, D = int(desc.n_kv_heads), int(desc.head_dim)
+    batch = int(desc.cache_batch_stride) or int(desc.cache_capacity) * H * D
+    for n, have, want in zip(t.shape, t.stride(), (batch, H * D, D, 1)):
+        if n > 1 and have != want:
+            raise ValueError(f"{name}: strides {tuple(t.stride())}, the descriptor says "
+                             f"{(batch, H * D, D, 1)}")
 
 
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -573,9 +586,9 @@ def _check_tokens(q, k, v, seqlens, out, lse, desc, stream=None):
     else:
         _need(lse, "lse", _f32, T * B * Hq, q, index)
     n = _cache_elems(B, desc)
-    _need_cache(k, "k", _BF16, n, q, index)
+    _need_cache(k, "k", _BF16, n, q, index, desc)
     if v is not None:
-        _need_cache(v, "v", _BF16, n, q, index)
+        _need_cache(v, "v", _BF16, n, q, index, desc)
     _need(seqlens, "seqlens", _i32, B, q, index)
     return T, B, index, out, lse
 
@@ -767,11 +780,11 @@ def _check_write(k_rows, v_rows, row_seq, row_slot, desc, k, v, dtypes):
     _need(row_slot, "row_slot", _i32, n_rows, k, index)
     stride = _row_stride(k_rows, "k_rows", desc, n_rows, k, index)
     n = _cache_elems(batch, desc)
-    _need_cache(k, "k", dtypes, n, k, index)
+    _need_cache(k, "k", dtypes, n, k, index, desc)
     if v_rows is not None and _row_stride(v_rows, "v_rows", desc, n_rows, k, index) != stride:
         raise ValueError("v_rows: must have the row stride of k_rows")
     if v is not None:
-        _need_cache(v, "v", dtypes, n, k, index)
+        _need_cache(v, "v", dtypes, n, k, index, desc)
     return n_rows, batch, stride
 
 

@@ -65,3 +65,32 @@ def test_more_rows_than_32_bits_count():
     for dtypes in (binding._BF16, binding._CODES):
         with pytest.raises(ValueError, match="at most"):
             binding._check_write(rows, rows, many, many, desc(), cache, cache, dtypes)
+
+
+# --------------------------------------------------------- caches that are views
+def by_sink(k, v, d):
+    binding._check_tokens(z(1, B, H, D), k, v, lens, None, None, d)
+
+
+def by_write(k, v, d):
+    binding._check_write(z(3, HKV, D), z(3, HKV, D), z(3, dtype=torch.int32),
+                         z(3, dtype=torch.int32), d, k, v, binding._BF16)
+
+
+@pytest.mark.parametrize("check", [by_sink, by_write])
+def test_views_of_caches_go_by_the_descriptor(check):
+    dense = z(B, C, HKV, D)
+    larger = z(B, C + 3, HKV, D)
+    part = larger[:, :C]
+    stride = (C + 3) * HKV * D
+    d = binding.make_desc(H, HKV, D, 4, 0.0, 1.0, False, C, stride)
+    check(dense, dense, desc())
+    check(part, part, d)
+    check(larger[1:, :C], larger[1:, :C], d) if check is by_write else None
+    for bad, dd in ((part, desc()),                                # the stride not given
+                    (z(B, HKV, C, D).transpose(1, 2), desc()),     # heads before slots
+                    (z(B, C, D, HKV).transpose(2, 3), desc()),
+                    (larger[:, ::2][:, :4].expand(B, 4, HKV, D), d)):
+        for k, v in ((bad, bad), (dense if dd is not d else part, bad)):
+            with pytest.raises(ValueError, match="strides|storage holds"):
+                check(k, v, dd)
