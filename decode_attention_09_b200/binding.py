@@ -819,7 +819,8 @@ def cache_write_fp8(k_rows: torch.Tensor, v_rows: Optional[torch.Tensor], row_se
                     v_codes: Optional[torch.Tensor], k_scale: torch.Tensor,
                     v_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """gdattn_cache_write_fp8: rows into the e4m3 caches [B, C, Hkv, D] (uint8 or
-    float8_e4m3fn) and their scales, fp32 [B, Hkv, C]."""
+    float8_e4m3fn) and their scales, fp32 [B, Hkv, C].  ``decode_fp8`` reads such a cache
+    in its own geometry and only when the slot map had no pinned slots (n_sink 0)."""
     n_rows, batch, stride = _check_write(k_rows, v_rows, row_seq, row_slot, desc, k_codes,
                                          v_codes, _CODES)
     index = k_codes.get_device()

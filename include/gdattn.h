@@ -459,10 +459,17 @@ gdattn_status gdattn_cache_write(const void *k_rows, const void *v_rows, int64_t
                                  void *v_cache, void *stream);
 
 /*
- * gdattn_cache_write into an fp8 cache (gdattn_decode_fp8 reads it): each row of
- * each KV head gets the scale s = max |x| / 448 and the codes e4m3(x / s), both
- * quotients rounded to fp32, the code to the nearest (ties to even); a row of
- * zeros gets scale 0 and codes 0.  Rows must be finite.
+ * gdattn_cache_write into an fp8 cache: each row of each KV head gets the scale
+ * s = max |x| / 448 and the codes e4m3(x / s), both quotients rounded to fp32, the
+ * code to the nearest (ties to even, a zero keeps its sign); a row of zeros gets
+ * scale 0 and codes 0.  Rows must be finite.
+ *
+ * Of what it writes this library reads one form itself: gdattn_decode_fp8 takes
+ * caches of its geometry (two query heads per KV head, head_dim 256, separate V)
+ * that were filled by a slot map without pinned slots (n_sink = 0, position j in
+ * slot j mod C).  A cache with pinned slots must not be passed to it: it has no way
+ * to tell, and would attend other rows.  Other geometries and pinned caches are for
+ * callers that keep or read such rows themselves.
  *
  *  k_codes, v_codes   e4m3 bytes; cache_batch_stride counts bytes and is a
  *                     multiple of 16
