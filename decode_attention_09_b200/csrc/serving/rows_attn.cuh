@@ -42,13 +42,17 @@
 //
 // What bounds it: a tile's softmax is a chain of some 4500 cycles (two reads of the
 // scores from tensor memory, the exponentials, the stores of the weights), the same for
-// one row and for 128, and two groups in turn give a tile every 2500 to 4000.  Its loops
+// one row and for 128, and two groups in turn give a tile every 2500 to 4000.  That comes
+// with query rows in the lanes: a block of one token has two live lanes of 128.  The
+// library's pair kernels, which put the cache rows there, take 17 us where this one takes
+// 22.6 (8 sequences, one token, windows of 1024) and 82 where it takes 108 to 123 (64).
+// With four tokens and up the two are even at 8 sequences (24), 89 to 125 at 64.  Its loops
 // take 16 columns and stay rolled, because all of the L1 is in use as shared memory and a
 // spilled register costs a trip to the L2: 32 or 64 columns at a time, or the next read in
-// flight, spill 100 to 560 bytes and take 10 to 25 % longer.  Measured: 64 sequences of 4
-// tokens over windows of 1024 in 130 us (4.2 TB/s), an 8192-token prompt in 238 us (540
-// TFLOP/s of the formula's products, half as many again with the weights' second part), 64
-// sequences behind 8192 shared tokens at head_dim 512 in 75 us.
+// flight, spill 100 to 560 bytes and take 10 to 25 % longer.  Measured: 64 ragged sequences of 4
+// tokens over windows of 1024 in 130 to 135 us (4.1 TB/s), an 8192-token prompt in 233 to
+// 242 us (540 TFLOP/s of the formula's products, half as many again with the weights'
+// second part), 64 sequences behind 8192 shared tokens at head_dim 512 in 75 to 78 us.
 //
 // A parity wait is sound only while its barrier is in the phase waited for or the
 // next.  kfull, vfull: eight uses back, tile i - 8's products are done.  odone of tile
